@@ -206,6 +206,122 @@ na_status na_forward_nd(const void *q, const void *k, const void *v, const void 
                         na_dtype dt, void *stream);
 
 /*
+ * Attention over packed sequences: what a model that mixes windowed and
+ * global layers runs in its global ones, over maps or prompts of unequal
+ * size in one call.  q, out: [total_q][heads_q][d]; k, v: [total_k][heads_k][d],
+ * heads_q a multiple of heads_k (query head h reads key head
+ * h / (heads_q / heads_k)).  cu_q, cu_k: nseq + 1 non-decreasing int32 on the
+ * device; sequence s owns the rows cu_q[s] .. cu_q[s+1] of q and the key slots
+ * cu_k[s] .. cu_k[s+1], of which the first len_k[s] hold keys (len_k NULL: all
+ * of them).  With Lq rows and Lk keys, row i stands at key position
+ * p = i + Lk - Lq, so that single tokens over a cache are sequences of one row;
+ *
+ *   causal = 0: row i sees keys 0 .. Lk-1;
+ *   causal = 1: it sees keys max(0, p-window+1) .. p (window = 0: from key 0);
+ *   s_ij = scale q_i . k_j,  P = softmax over the keys seen,  out_i = sum_j P_ij v_j,
+ *   lse[h][i] = ln sum_j e^(s_ij), float32 [heads_q][total_q] (NULL: not written).
+ *
+ * A row that sees no key gets zeros and an lse of -inf.  Keys that a row does
+ * not see, slots past len_k and other sequences never reach its result,
+ * whatever they hold (NaN and infinities too).  Rows of q that belong to no
+ * sequence are left as they were in out and lse.  The lengths are read on the
+ * device and clamped to the tensors, so a captured call can be replayed with
+ * other lengths in the same buffers.
+ *
+ * Softmax statistics and sums are float32; 16-bit types round the weights to
+ * dt for the weighted sum.  d in {16, 32, 64, 128}; scale > 0; window >= 0,
+ * and 0 unless causal; total_q, total_k <= 2^30, heads_k <= 65535 and
+ * (total_q + total_k) * heads_q * d < 2^40 (more: NA_ERR_UNSUPPORTED).
+ * workspace: a 256-byte aligned device buffer of at least na_packed_workspace_bytes() bytes (may be
+ * 0); calls that may run at the same time need one each.
+ * NULL is allowed for k and v when total_k is 0.
+ */
+size_t na_packed_workspace_bytes(int nseq, int total_q, int total_k, int heads_q, int heads_k, int d, na_dtype dt);
+na_status na_packed_forward(const void *q, const void *k, const void *v, const int *cu_q, const int *cu_k,
+                            const int *len_k, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                            int nseq, int total_q, int total_k, int heads_q, int heads_k, int d, int causal,
+                            int window, float scale, na_dtype dt, void *stream);
+
+/*
+ * Backward of na_packed_forward: with out and lse as the forward left them and
+ * dout the gradient of out,
+ *
+ *   P_ij = e^(s_ij - lse_i),  dS_ij = P_ij (dout_i . v_j - dout_i . out_i),
+ *   dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,  dv_j = sum_i P_ij dout_i,
+ *
+ * dk and dv summed over the heads of the group too.  Arguments as the
+ * forward's; every key slot belongs to the sequence (there is no len_k).
+ * dq, dk and dv are written, not added to; rows of no sequence are left as
+ * they were.  Each gradient is summed in a fixed order, so a call's results
+ * do not vary from run to run.  workspace: 256-byte aligned, at least
+ * na_packed_backward_workspace_bytes() bytes.
+ */
+size_t na_packed_backward_workspace_bytes(int nseq, int total_q, int total_k, int heads_q, int heads_k, int d,
+                                          na_dtype dt);
+na_status na_packed_backward(const void *q, const void *k, const void *v, const void *out, const float *lse,
+                             const void *dout, const int *cu_q, const int *cu_k, void *dq, void *dk, void *dv,
+                             void *workspace, size_t workspace_bytes, int nseq, int total_q, int total_k,
+                             int heads_q, int heads_k, int d, int causal, int window, float scale, na_dtype dt,
+                             void *stream);
+
+/*
+ * The norms around a block, with its gate and residual, in one pass:
+ *
+ *   y = x + scale * gate . P(o),   h = N(y) w + b.
+ *
+ * x (the residual), o (the block's output), y, h: [rows][C].  N is a
+ * LayerNorm (rms = 0) or an RMS norm (rms = 1) over the C channels with eps
+ * added to the variance or mean square; P is N with weight post_w and bias
+ * post_b (post = 1) or the identity (post = 0).  gate: [gates][C], rows / gates
+ * consecutive rows a gate row (1: one for all, as a layer scale; B: one per map
+ * of a batch), or NULL with gates = 0 (no gate).  w, b, post_w, post_b: [C] or
+ * NULL (1, 0).  All of type dt, 16-byte aligned.
+ *
+ * o and y NULL: only h = N(x) w + b.  h NULL (w and b too): only y.  y may be
+ * x and h may be o (a call reads a row before it writes it); no other
+ * overlaps.  Statistics are float32, and h comes from y before its rounding to
+ * dt.  rows * C < 2^40, C <= 8192 (more: NA_ERR_UNSUPPORTED).  rows = 0 is a
+ * no-op.
+ */
+na_status na_norm_forward(const void *x, const void *o, const void *post_w, const void *post_b, const void *gate,
+                          const void *w, const void *b, void *y, void *h, long long rows, int C, long long gates,
+                          int rms, int post, float eps, float scale, na_dtype dt, void *stream);
+
+/*
+ * Backward of na_norm_forward.  y is the forward's y (its x where o was NULL),
+ * dy and dh the gradients of y and h (either may be NULL: zero).  Writes dx,
+ * and d_o where o is given, in dt; the gradients of the weights in float32:
+ * dw, db, dpost_w, dpost_b [C], dgate [gates][C], each NULL to skip it.
+ * N(y) is recomputed from the y that was rounded to dt.  dx may be dy, and d_o
+ * may be o or dh; no other overlaps.  Sums over rows are in a fixed order.
+ * workspace: 256-byte aligned, at least na_norm_backward_workspace_bytes()
+ * bytes.  rows = 0 is NA_ERR_UNSUPPORTED.
+ */
+size_t na_norm_backward_workspace_bytes(long long rows, int C, long long gates, na_dtype dt);
+na_status na_norm_backward(const void *y, const void *o, const void *post_w, const void *post_b, const void *gate,
+                           const void *w, const void *dy, const void *dh, void *dx, void *d_o, float *dw, float *db,
+                           float *dpost_w, float *dpost_b, float *dgate, void *workspace, size_t workspace_bytes,
+                           long long rows, int C, long long gates, int rms, int post, float eps, float scale,
+                           na_dtype dt, void *stream);
+
+/*
+ * The attention half of a NAT layer, the norms and the residual around
+ * na2d_block_forward:
+ *
+ *   y = x + scale * gate . P(block(N(x) w + b)),
+ *
+ * N, P and gate as in na_norm_forward (gates divides B*H*W), the block's
+ * arguments as in na2d_block_forward.  y may be x.  workspace: 256-byte
+ * aligned, at least na2d_layer_workspace_bytes() bytes.
+ */
+size_t na2d_layer_workspace_bytes(int B, int H, int W, int heads, int dh, int ksize, na_dtype dt);
+na_status na2d_layer_forward(const void *x, const void *w, const void *b, const void *wqkv, const void *bqkv,
+                             const void *wo, const void *bo, const void *rpb, const void *post_w,
+                             const void *post_b, const void *gate, void *y, void *workspace,
+                             size_t workspace_bytes, int B, int H, int W, int heads, int dh, int ksize, int gates,
+                             int rms, int post, float eps, float scale, na_dtype dt, void *stream);
+
+/*
  * na2d_forward from HOST buffers: copies q, k, v (and rpb when not NULL)
  * host-to-device into the caller's device workspace, runs na2d_forward and
  * copies the result back to out_host, one cudaMemcpyAsync per buffer and

@@ -86,6 +86,8 @@ __global__ void timeout_probe_kernel(unsigned* status, unsigned long long limit_
 }  // namespace
 }  // namespace na2d
 
+cudaError_t na2d::status_word(unsigned** out) { return status_ptr(out); }
+
 using namespace na2d;
 
 NA_EXPORT const char* na_status_str(na_status s) {

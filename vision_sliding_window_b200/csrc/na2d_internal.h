@@ -53,6 +53,51 @@ cudaError_t launch_forward_nd(const void* q, const void* k, const void* v, const
                               int heads, const int (&L)[3], int d, const int (&ks)[3], const int (&dil)[3],
                               na_dtype dt, cudaStream_t st);
 
+// Device address of the current device's status word (na2d_api.cu).
+cudaError_t status_word(unsigned** out);
+
+// Norms around a block (na_norm.cu).
+struct NormArgs {
+  const void *x, *o, *pw, *pb, *gate, *w, *b;  // x is y in the backward pass
+  void *y, *h;
+  const void *dy, *dh;
+  void *dx, *dout;  // dout: the gradient of o
+  float *dw, *db, *dpw, *dpb, *dgate, *partial;
+  long long rows, gate_rows;  // gate_rows rows share a row of the gate
+  int C, rms, post;
+  float eps, scale;
+  int lanes, pieces;  // set by the launchers
+  long long chunks, chunk_rows;
+};
+size_t norm_workspace_bytes(long long rows, int C, long long gate_rows);
+cudaError_t launch_norm_forward(const NormArgs& p, na_dtype dt, cudaStream_t st);
+cudaError_t launch_norm_backward(NormArgs p, na_dtype dt, cudaStream_t st);
+
+// Attention over packed sequences (na_packed_*.cu).
+struct PackedArgs {
+  const void *q, *k, *v;
+  void* out;
+  float* lse;
+  const int *cu_q, *cu_k, *len_k;
+  const void *o, *dout;  // backward: the forward's output and its gradient
+  const float* lse_in;
+  void *dq, *dk, *dv;
+  int nseq, total_q, total_k, hq, hk, group, d, causal, window;
+  float scale;
+  // keys of a piece when a sequence's keys are cut into pieces that are
+  // joined afterwards (0: not cut), and the pieces' results
+  int piece_keys, max_pieces;
+  float *part_o, *part_lse;  // [max_pieces][total_q][hq][d] and [max_pieces][total_q][hq]
+  float* delta;              // backward: [total_q][hq]
+  unsigned* status;
+};
+// Sets piece_keys and max_pieces, from sizes alone (na_packed_simt.cu).
+void packed_set_pieces(PackedArgs* p, bool tc);
+size_t packed_workspace_bytes(const PackedArgs& p, na_dtype dt);
+size_t packed_backward_workspace_bytes(const PackedArgs& p);
+cudaError_t launch_packed_forward(PackedArgs p, void* workspace, na_dtype dt, cudaStream_t st);
+cudaError_t launch_packed_backward(PackedArgs p, void* workspace, na_dtype dt, cudaStream_t st);
+
 // Tensor-core fused forward (na2d_tc.cu), fp16/bf16.
 bool forward_tc_supported(const Shape& s, na_dtype dt);
 cudaError_t launch_forward_tc(const void* q, const void* k, const void* v, const void* rpb,

@@ -1,0 +1,642 @@
+// na_packed_simt.cu -- attention over packed sequences on the CUDA cores, its
+// gradients, and the join of partial results; for float32, and for the shapes
+// that the tensor-core kernels do not take.
+//
+// Forward.  A block owns kRows rows (one key head's) and walks the keys they
+// see in tiles of 64 with a running maximum and sum; S and the output stay in
+// registers, each thread a 4 x 8 patch of S and 4 rows x d/8 columns of the
+// output, fed from float32 tiles in shared memory by 16-byte loads: 128 FMAs
+// for 12 loads in S, so FMA issue bounds it, not shared memory.  With few
+// rows (single tokens) 16-row tiles waste less of a tile.
+//
+// Backward.  P and dS are recomputed from the rows' log-sum-exp, once with a
+// block owning 64 keys (dk, dv) and once with a block owning 64 rows (dq): two
+// more products than one kernel that adds dq with atomics, but each gradient
+// is one block's sum in a fixed order.
+//
+// A product never touches a masked entry: weights of masked places are
+// skipped, not multiplied by zero, so that what they hold (NaN, infinities)
+// cannot reach a result.
+#include <type_traits>
+
+#include "na_packed.cuh"
+
+namespace na2d {
+namespace {
+
+using namespace packed;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kKeys = 64;  // keys of a tile
+constexpr int kThreads = 128;
+
+template <typename T> NA_DEVICE float to_f(T x);
+template <> NA_DEVICE float to_f<float>(float x) { return x; }
+template <> NA_DEVICE float to_f<__half>(__half x) { return __half2float(x); }
+template <> NA_DEVICE float to_f<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T> NA_DEVICE T from_f(float x);
+template <> NA_DEVICE float from_f<float>(float x) { return x; }
+template <> NA_DEVICE __half from_f<__half>(float x) { return __float2half_rn(x); }
+template <> NA_DEVICE __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// Loads `n` vectors' worth of a row of D elements into shared float32.
+template <typename T, int D> NA_DEVICE void load_vec(const T* g, float* s, int v, bool live) {
+  constexpr int VEC = 16 / sizeof(T);
+  float f[VEC];
+  if (live) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(g) + v);
+    const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) f[i] = to_f<T>(e[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) f[i] = 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < VEC; i += 4)
+    *reinterpret_cast<float4*>(s + v * VEC + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+}
+
+template <int D> struct Tile {
+  static constexpr int LD = D + 4;  // floats a staged row: 16-byte loads of 8 rows fall on distinct banks
+  static constexpr int CPT = D / 8;  // output columns a thread
+  static constexpr int CV = CPT >= 4 ? 4 : CPT;  // of which this many are consecutive
+};
+
+// Rows [r0, r0 + n) of one key head's rows of a sequence (position r / G, head
+// r % G) from a tensor [total_q][hq][D].
+template <typename T, int D>
+NA_DEVICE void load_rows(const PackedArgs& p, const Span& sp, const T* g, int kh, long long r0, int n, int rows,
+                         float* s) {
+  constexpr int VPR = D * sizeof(T) / 16;
+  for (int e = threadIdx.x; e < rows * VPR; e += kThreads) {
+    const int r = e / VPR, v = e % VPR;
+    const bool live = r < n;
+    const long long rr = live ? r0 + r : r0;
+    const long long at = ((long long)sp.q0 + rr / p.group) * p.hq + kh * p.group + rr % p.group;
+    load_vec<T, D>(g + at * D, s + r * Tile<D>::LD, v, live);
+  }
+}
+template <typename T, int D>
+NA_DEVICE void load_keys(const PackedArgs& p, const Span& sp, const T* g, int kh, int k0, int n, float* s) {
+  constexpr int VPR = D * sizeof(T) / 16;
+  for (int e = threadIdx.x; e < kKeys * VPR; e += kThreads) {
+    const int j = e / VPR, v = e % VPR;
+    const bool live = j < n;
+    const long long at = ((long long)sp.k0 + (live ? k0 + j : k0)) * p.hk + kh;
+    load_vec<T, D>(g + at * D, s + j * Tile<D>::LD, v, live);
+  }
+}
+
+// c[r][j] = a row (ty R + r) . b row (tx + 8 j) of two staged tiles
+template <int D, int R>
+NA_DEVICE void dot_patch(const float* a, const float* b, int ty, int tx, float (&c)[R][8]) {
+  constexpr int LD = Tile<D>::LD;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c[r][j] = 0.f;
+#pragma unroll 4
+  for (int d = 0; d < D; d += 4) {
+    float4 x[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) x[r] = *reinterpret_cast<const float4*>(a + (ty * R + r) * LD + d);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float4 y = *reinterpret_cast<const float4*>(b + (tx + 8 * j) * LD + d);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        c[r][j] = fmaf(x[r].x, y.x, c[r][j]);
+        c[r][j] = fmaf(x[r].y, y.y, c[r][j]);
+        c[r][j] = fmaf(x[r].z, y.z, c[r][j]);
+        c[r][j] = fmaf(x[r].w, y.w, c[r][j]);
+      }
+    }
+  }
+}
+
+// acc[r][.] += w[ty R + r][j] * b[j][this thread's columns] for j in [0, n)
+// with j inside row r's [lo, hi)
+template <int D, int R, int WLD>
+NA_DEVICE void weighted_sum(const float* w, const float* b, int ty, int tx, int n, const int (&lo)[R],
+                            const int (&hi)[R], float (&acc)[R][Tile<D>::CPT]) {
+  constexpr int LD = Tile<D>::LD, CPT = Tile<D>::CPT, CV = Tile<D>::CV;
+  for (int j = 0; j < n; ++j) {
+    float v[CPT];
+#pragma unroll
+    for (int c = 0; c < CPT / CV; ++c) {
+      const float* from = b + j * LD + c * 8 * CV + tx * CV;
+      if constexpr (CV == 4) {
+        const float4 f = *reinterpret_cast<const float4*>(from);
+        v[4 * c] = f.x, v[4 * c + 1] = f.y, v[4 * c + 2] = f.z, v[4 * c + 3] = f.w;
+      } else {
+        const float2 f = *reinterpret_cast<const float2*>(from);
+        v[0] = f.x, v[1] = f.y;
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float x = w[(ty * R + r) * WLD + j];
+      if (j >= lo[r] && j < hi[r])
+#pragma unroll
+        for (int c = 0; c < CPT; ++c) acc[r][c] = fmaf(x, v[c], acc[r][c]);
+    }
+  }
+}
+
+template <typename T, int D, int R>
+NA_DEVICE void store_cols(T* g, int tx, const float (&acc)[Tile<D>::CPT], float f) {
+  constexpr int CPT = Tile<D>::CPT, CV = Tile<D>::CV;
+#pragma unroll
+  for (int c = 0; c < CPT; ++c) g[(c / CV) * 8 * CV + tx * CV + c % CV] = from_f<T>(acc[c] * f);
+}
+
+template <int D, int R> constexpr int fwd_smem() {
+  return (16 * R * Tile<D>::LD + 2 * kKeys * Tile<D>::LD + 16 * R * (kKeys + 1)) * (int)sizeof(float);
+}
+
+// ----------------------------------------------------------------- forward
+template <typename T, int D, int R>
+__global__ void __launch_bounds__(kThreads) packed_forward_simt_kernel(PackedArgs p) {
+  constexpr int ROWS = 16 * R, LD = Tile<D>::LD, CPT = Tile<D>::CPT;
+  extern __shared__ __align__(16) float sm[];
+  float* Qs = sm;
+  float* Ks = Qs + ROWS * LD;
+  float* Vs = Ks + kKeys * LD;
+  float* Ps = Vs + kKeys * LD;
+  const int ty = threadIdx.x / 8, tx = threadIdx.x % 8;
+  const int kh = blockIdx.y;
+  const float sl2 = p.scale * kLog2e;
+  int s;
+  long long idx;
+  const bool split = p.piece_keys > 0;
+  if (split)
+    find_part(p.cu_k, p.nseq, p.total_k, 1, p.piece_keys, blockIdx.x, &s, &idx);
+  else
+    find_part(p.cu_q, p.nseq, p.total_q, p.group, ROWS, blockIdx.x, &s, &idx);
+  if (idx < 0) return;
+  const Span sp = span_of(p, s);
+  const long long all_rows = (long long)sp.nq * p.group;
+  int piece0 = 0, piece1 = sp.nk;
+  long long t0 = idx, t1 = idx + 1;
+  if (split) {
+    if (idx >= p.max_pieces || idx * p.piece_keys >= sp.nk) return;
+    piece0 = (int)idx * p.piece_keys;
+    piece1 = min(piece0 + p.piece_keys, sp.nk);
+    t0 = 0;
+    t1 = (all_rows + ROWS - 1) / ROWS;
+  }
+  for (long long t = t0; t < t1; ++t) {
+    const long long r0 = t * ROWS;
+    if (r0 >= all_rows) return;
+    const int n = (int)min((long long)ROWS, all_rows - r0);
+    int lo[R], hi[R], kb, ke, unused;
+    visible(p, sp, (int)(r0 / p.group), &kb, &unused);
+    visible(p, sp, (int)((r0 + n - 1) / p.group), &unused, &ke);
+    kb = max(kb, piece0);
+    ke = min(ke, piece1);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int row = ty * R + r;
+      visible(p, sp, (int)((r0 + min(row, n - 1)) / p.group), &lo[r], &hi[r]);
+      if (row >= n) hi[r] = lo[r];
+    }
+    __syncthreads();
+    load_rows<T, D>(p, sp, (const T*)p.q, kh, r0, n, ROWS, Qs);
+    float m[R], l[R], acc[R][CPT];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+#pragma unroll
+      for (int c = 0; c < CPT; ++c) acc[r][c] = 0.f;
+    }
+    for (int k0 = kb; k0 < ke; k0 += kKeys) {
+      const int nk = min(kKeys, ke - k0);
+      __syncthreads();
+      load_keys<T, D>(p, sp, (const T*)p.k, kh, k0, nk, Ks);
+      load_keys<T, D>(p, sp, (const T*)p.v, kh, k0, nk, Vs);
+      __syncthreads();
+      float sc[R][8];
+      dot_patch<D, R>(Qs, Ks, ty, tx, sc);
+      int tlo[R], thi[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        tlo[r] = lo[r] - k0;
+        thi[r] = min(hi[r] - k0, nk);
+        float mx = m[r];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int key = tx + 8 * j;
+          if (!(key >= tlo[r] && key < thi[r])) sc[r][j] = -INFINITY;
+          mx = fmaxf(mx, sc[r][j]);
+        }
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float ref = mx == -INFINITY ? 0.f : mx * sl2;
+        const float f = exp2f(fmaf(m[r], sl2, -ref));
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float e = exp2f(fmaf(sc[r][j], sl2, -ref));
+          sum += e;
+          Ps[(ty * R + r) * (kKeys + 1) + tx + 8 * j] = e;
+        }
+        l[r] = fmaf(l[r], f, sum);
+        m[r] = mx;
+#pragma unroll
+        for (int c = 0; c < CPT; ++c) acc[r][c] *= f;
+      }
+      __syncwarp();
+      weighted_sum<D, R, kKeys + 1>(Ps, Vs, ty, tx, nk, tlo, thi, acc);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float sum = l[r];
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      const int row = ty * R + r;
+      if (row >= n) continue;
+      const long long rr = r0 + row;
+      const long long i = (long long)sp.q0 + rr / p.group;
+      const int head = kh * p.group + (int)(rr % p.group);
+      // a row that saw no key: zeros and -inf
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const float lse = sum == 0.f ? -INFINITY : fmaf(m[r], p.scale, log2f(sum) * kLn2);
+      if (split) {
+        const long long at = (idx * p.total_q + i) * p.hq + head;
+        store_cols<float, D, R>(p.part_o + at * D, tx, acc[r], inv);
+        if (tx == 0) p.part_lse[at] = lse;
+      } else {
+        store_cols<T, D, R>((T*)p.out + (i * p.hq + head) * D, tx, acc[r], inv);
+        if (tx == 0 && p.lse) p.lse[(long long)head * p.total_q + i] = lse;
+      }
+    }
+  }
+}
+
+// Joins the pieces of every row: out = sum_c e^(lse_c - lse) o_c.  One warp a
+// row; rows behind the last sequence belong to none and are left alone.
+template <typename T>
+__global__ void __launch_bounds__(256) packed_join_kernel(PackedArgs p) {
+  const int lane = threadIdx.x & 31;
+  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= (long long)p.total_q * p.hq) return;
+  const int i = (int)(row / p.hq), head = (int)(row % p.hq);
+  int a = 0, b = p.nseq - 1;  // the last sequence that starts at or before i
+  while (a < b) {
+    const int mid = (a + b + 1) >> 1;
+    if (clamped(p.cu_q, mid, p.total_q) <= i)
+      a = mid;
+    else
+      b = mid - 1;
+  }
+  const Span sp = span_of(p, a);
+  if (i < sp.q0 || i >= sp.q0 + sp.nq) return;
+  int lo, hi;
+  visible(p, sp, i - sp.q0, &lo, &hi);
+  const int c0 = lo / p.piece_keys, c1 = lo < hi ? min((hi - 1) / p.piece_keys + 1, p.max_pieces) : c0;
+  const long long step = (long long)p.total_q * p.hq;
+  float mx = -INFINITY;
+  for (int c = c0 + lane; c < c1; c += 32) mx = fmaxf(mx, p.part_lse[c * step + row]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  const float ref = mx == -INFINITY ? 0.f : mx;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
+  for (int c = c0; c < c1; ++c) {
+    const float w = expf(p.part_lse[c * step + row] - ref);
+    sum += w;
+    if (w == 0.f) continue;  // a piece of which the row saw nothing
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (lane + 32 * e < p.d) acc[e] = fmaf(w, p.part_o[(c * step + row) * p.d + lane + 32 * e], acc[e]);
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (lane + 32 * e < p.d) ((T*)p.out)[row * p.d + lane + 32 * e] = from_f<T>(acc[e] * inv);
+  if (lane == 0 && p.lse) p.lse[(long long)head * p.total_q + i] = sum == 0.f ? -INFINITY : ref + logf(sum);
+}
+
+// ---------------------------------------------------------------- backward
+// delta = out . dout for every row, [total_q][hq]
+template <typename T, int D> __global__ void __launch_bounds__(256) packed_delta_kernel(PackedArgs p) {
+  constexpr int VEC = 16 / sizeof(T), LPR = D / VEC;  // lanes a row
+  const long long row = ((long long)blockIdx.x * 256 + threadIdx.x) / LPR;
+  const int v = threadIdx.x % LPR;
+  const bool live = row < (long long)p.total_q * p.hq;
+  float s = 0.f;
+  if (live) {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p.o) + row * LPR + v);
+    const uint4 b = __ldg(reinterpret_cast<const uint4*>(p.dout) + row * LPR + v);
+    const T *x = reinterpret_cast<const T*>(&a), *y = reinterpret_cast<const T*>(&b);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) s = fmaf(to_f<T>(x[i]), to_f<T>(y[i]), s);
+  }
+#pragma unroll
+  for (int o = 1; o < LPR; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (live && v == 0) p.delta[row] = s;
+}
+
+template <int D> constexpr int bwd_smem() {
+  return (4 * kKeys * Tile<D>::LD + 2 * kKeys * (kKeys + 1) + 2 * kKeys) * (int)sizeof(float);
+}
+
+// lse (in units of log2) and delta of the staged rows
+NA_DEVICE void load_row_terms(const PackedArgs& p, const Span& sp, int kh, long long r0, int n, float* lse,
+                              float* delta) {
+  if (threadIdx.x < kKeys) {
+    const int r = threadIdx.x;
+    const long long rr = r0 + (r < n ? r : 0);
+    const long long i = (long long)sp.q0 + rr / p.group;
+    const int head = kh * p.group + (int)(rr % p.group);
+    lse[r] = p.lse_in[(long long)head * p.total_q + i] * kLog2e;
+    delta[r] = p.delta[i * p.hq + head];
+  }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) packed_dkdv_simt_kernel(PackedArgs p) {
+  constexpr int R = 4, LD = Tile<D>::LD, CPT = Tile<D>::CPT, WLD = kKeys + 1;
+  extern __shared__ __align__(16) float sm[];
+  float* Ks = sm;
+  float* Vs = Ks + kKeys * LD;
+  float* Qs = Vs + kKeys * LD;
+  float* Os = Qs + kKeys * LD;
+  float* Ps = Os + kKeys * LD;
+  float* Ss = Ps + kKeys * WLD;
+  float* lse = Ss + kKeys * WLD;
+  float* delta = lse + kKeys;
+  const int ty = threadIdx.x / 8, tx = threadIdx.x % 8;
+  const int kh = blockIdx.y;
+  const float sl2 = p.scale * kLog2e;
+  int s;
+  long long idx;
+  find_part(p.cu_k, p.nseq, p.total_k, 1, kKeys, blockIdx.x, &s, &idx);
+  if (idx < 0) return;
+  const Span sp = span_of(p, s);
+  if (idx * kKeys >= sp.nk) return;
+  const int j0 = (int)idx * kKeys, nk = min(kKeys, sp.nk - j0);
+  load_keys<T, D>(p, sp, (const T*)p.k, kh, j0, nk, Ks);
+  load_keys<T, D>(p, sp, (const T*)p.v, kh, j0, nk, Vs);
+  long long lo[R], hi[R];  // rows that see this thread's keys
+  int a, b;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int j = ty * R + r;
+    seen_by(p, sp, j0 + min(j, nk - 1), &a, &b);
+    lo[r] = (long long)a * p.group;
+    hi[r] = j < nk ? (long long)b * p.group : lo[r];
+  }
+  float dk[R][CPT], dv[R][CPT];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int c = 0; c < CPT; ++c) dk[r][c] = dv[r][c] = 0.f;
+  int unused, first, last;
+  seen_by(p, sp, j0, &first, &unused);
+  seen_by(p, sp, j0 + nk - 1, &unused, &last);
+  for (long long r0 = (long long)first * p.group; r0 < (long long)last * p.group; r0 += kKeys) {
+    const int n = (int)min((long long)kKeys, (long long)last * p.group - r0);
+    __syncthreads();
+    load_rows<T, D>(p, sp, (const T*)p.q, kh, r0, n, kKeys, Qs);
+    load_rows<T, D>(p, sp, (const T*)p.dout, kh, r0, n, kKeys, Os);
+    load_row_terms(p, sp, kh, r0, n, lse, delta);
+    __syncthreads();
+    float sc[R][8], dp[R][8];
+    dot_patch<D, R>(Ks, Qs, ty, tx, sc);
+    dot_patch<D, R>(Vs, Os, ty, tx, dp);
+    int tlo[R], thi[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      tlo[r] = (int)max(lo[r] - r0, 0ll);
+      thi[r] = (int)min(max(hi[r] - r0, 0ll), (long long)n);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int row = tx + 8 * j;
+        const float e = exp2f(fmaf(sc[r][j], sl2, -lse[row]));
+        Ps[(ty * R + r) * WLD + row] = e;
+        Ss[(ty * R + r) * WLD + row] = e * (dp[r][j] - delta[row]);
+      }
+    }
+    __syncwarp();
+    weighted_sum<D, R, WLD>(Ps, Os, ty, tx, n, tlo, thi, dv);
+    weighted_sum<D, R, WLD>(Ss, Qs, ty, tx, n, tlo, thi, dk);
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int j = ty * R + r;
+    if (j >= nk) continue;
+    const long long at = ((long long)(sp.k0 + j0 + j) * p.hk + kh) * D;
+    store_cols<T, D, R>((T*)p.dk + at, tx, dk[r], p.scale);
+    store_cols<T, D, R>((T*)p.dv + at, tx, dv[r], 1.f);
+  }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) packed_dq_simt_kernel(PackedArgs p) {
+  constexpr int R = 4, LD = Tile<D>::LD, CPT = Tile<D>::CPT, WLD = kKeys + 1, ROWS = 64;
+  extern __shared__ __align__(16) float sm[];
+  float* Ks = sm;
+  float* Vs = Ks + kKeys * LD;
+  float* Qs = Vs + kKeys * LD;
+  float* Os = Qs + kKeys * LD;
+  float* Ss = Os + kKeys * LD;
+  float* lse = Ss + 2 * kKeys * WLD;
+  float* delta = lse + kKeys;
+  const int ty = threadIdx.x / 8, tx = threadIdx.x % 8;
+  const int kh = blockIdx.y;
+  const float sl2 = p.scale * kLog2e;
+  int s;
+  long long idx;
+  find_part(p.cu_q, p.nseq, p.total_q, p.group, ROWS, blockIdx.x, &s, &idx);
+  if (idx < 0) return;
+  const Span sp = span_of(p, s);
+  const long long all_rows = (long long)sp.nq * p.group, r0 = idx * ROWS;
+  if (r0 >= all_rows) return;
+  const int n = (int)min((long long)ROWS, all_rows - r0);
+  load_rows<T, D>(p, sp, (const T*)p.q, kh, r0, n, ROWS, Qs);
+  load_rows<T, D>(p, sp, (const T*)p.dout, kh, r0, n, ROWS, Os);
+  load_row_terms(p, sp, kh, r0, n, lse, delta);
+  int lo[R], hi[R], kb, ke, unused;
+  visible(p, sp, (int)(r0 / p.group), &kb, &unused);
+  visible(p, sp, (int)((r0 + n - 1) / p.group), &unused, &ke);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int row = ty * R + r;
+    visible(p, sp, (int)((r0 + min(row, n - 1)) / p.group), &lo[r], &hi[r]);
+    if (row >= n) hi[r] = lo[r];
+  }
+  float dq[R][CPT];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int c = 0; c < CPT; ++c) dq[r][c] = 0.f;
+  for (int k0 = kb; k0 < ke; k0 += kKeys) {
+    const int nk = min(kKeys, ke - k0);
+    __syncthreads();
+    load_keys<T, D>(p, sp, (const T*)p.k, kh, k0, nk, Ks);
+    load_keys<T, D>(p, sp, (const T*)p.v, kh, k0, nk, Vs);
+    __syncthreads();
+    float sc[R][8], dp[R][8];
+    dot_patch<D, R>(Qs, Ks, ty, tx, sc);
+    dot_patch<D, R>(Os, Vs, ty, tx, dp);
+    int tlo[R], thi[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      tlo[r] = lo[r] - k0;
+      thi[r] = min(hi[r] - k0, nk);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        Ss[(ty * R + r) * WLD + tx + 8 * j] =
+            exp2f(fmaf(sc[r][j], sl2, -lse[ty * R + r])) * (dp[r][j] - delta[ty * R + r]);
+    }
+    __syncwarp();
+    weighted_sum<D, R, WLD>(Ss, Ks, ty, tx, nk, tlo, thi, dq);
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int row = ty * R + r;
+    if (row >= n) continue;
+    const long long rr = r0 + row;
+    const long long at = ((long long)sp.q0 + rr / p.group) * p.hq + kh * p.group + rr % p.group;
+    store_cols<T, D, R>((T*)p.dq + at * D, tx, dq[r], p.scale);
+  }
+}
+
+// ---------------------------------------------------------------- launches
+template <typename K> cudaError_t with_smem(K kern, int bytes) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+bool few_rows(const PackedArgs& p) { return (long long)p.total_q * p.group <= 16ll * p.nseq; }
+
+template <typename T, int D, int R> cudaError_t forward_r(const PackedArgs& p, cudaStream_t st) {
+  const long long blocks = p.piece_keys > 0 ? part_numbers(p.nseq, p.total_k, 1, p.piece_keys)
+                                            : part_numbers(p.nseq, p.total_q, p.group, 16 * R);
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  auto kern = packed_forward_simt_kernel<T, D, R>;
+  cudaError_t e = with_smem(kern, fwd_smem<D, R>());
+  if (e != cudaSuccess) return e;
+  kern<<<dim3((unsigned)blocks, (unsigned)p.hk), kThreads, fwd_smem<D, R>(), st>>>(p);
+  return cudaGetLastError();
+}
+template <typename T, int D> cudaError_t forward_d(const PackedArgs& p, cudaStream_t st) {
+  return few_rows(p) ? forward_r<T, D, 1>(p, st) : forward_r<T, D, 4>(p, st);
+}
+template <typename T> cudaError_t forward_t(const PackedArgs& p, cudaStream_t st) {
+  switch (p.d) {
+    case 16: return forward_d<T, 16>(p, st);
+    case 32: return forward_d<T, 32>(p, st);
+    case 64: return forward_d<T, 64>(p, st);
+    case 128: return forward_d<T, 128>(p, st);
+  }
+  return cudaErrorInvalidValue;
+}
+template <typename T, int D> cudaError_t backward_d(const PackedArgs& p, cudaStream_t st) {
+  const long long kb = part_numbers(p.nseq, p.total_k, 1, kKeys), qb = part_numbers(p.nseq, p.total_q, p.group, 64);
+  if (kb > 0x7fffffffLL || qb > 0x7fffffffLL) return cudaErrorInvalidValue;
+  cudaError_t e = with_smem(packed_dkdv_simt_kernel<T, D>, bwd_smem<D>());
+  if (e == cudaSuccess) e = with_smem(packed_dq_simt_kernel<T, D>, bwd_smem<D>());
+  if (e != cudaSuccess) return e;
+  packed_dkdv_simt_kernel<T, D><<<dim3((unsigned)kb, (unsigned)p.hk), kThreads, bwd_smem<D>(), st>>>(p);
+  packed_dq_simt_kernel<T, D><<<dim3((unsigned)qb, (unsigned)p.hk), kThreads, bwd_smem<D>(), st>>>(p);
+  return cudaGetLastError();
+}
+template <typename T> cudaError_t backward_t(const PackedArgs& p, cudaStream_t st) {
+  switch (p.d) {
+    case 16: return backward_d<T, 16>(p, st);
+    case 32: return backward_d<T, 32>(p, st);
+    case 64: return backward_d<T, 64>(p, st);
+    case 128: return backward_d<T, 128>(p, st);
+  }
+  return cudaErrorInvalidValue;
+}
+template <typename T, int D> cudaError_t delta_d(const PackedArgs& p, cudaStream_t st) {
+  constexpr int kRows = 256 * 16 / ((int)sizeof(T) * D);
+  const long long rows = (long long)p.total_q * p.hq, blocks = (rows + kRows - 1) / kRows;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  packed_delta_kernel<T, D><<<(unsigned)blocks, 256, 0, st>>>(p);
+  return cudaGetLastError();
+}
+template <typename T> cudaError_t delta_t(const PackedArgs& p, cudaStream_t st) {
+  switch (p.d) {
+    case 16: return delta_d<T, 16>(p, st);
+    case 32: return delta_d<T, 32>(p, st);
+    case 64: return delta_d<T, 64>(p, st);
+    case 128: return delta_d<T, 128>(p, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+template <typename T> cudaError_t join_t(const PackedArgs& p, cudaStream_t st) {
+  const long long blocks = ((long long)p.total_q * p.hq + 7) / 8;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  packed_join_kernel<T><<<(unsigned)blocks, 256, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+// One call of a template for each element type.
+template <typename F> cudaError_t by_type(na_dtype dt, F f) {
+  if (dt == NA_F32) return f(float{});
+  if (dt == NA_F16) return f(__half{});
+  return f(__nv_bfloat16{});
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace
+
+// The keys are cut when the row tiles alone leave SMs idle: single tokens,
+// and short prompts over long caches.  Pieces are as long as leaves about
+// kWant blocks, not under kLeast keys (each piece's rows pay for writing and
+// joining a float32 output), and a cut pays only where a sequence of average
+// length spans several.
+void packed_set_pieces(PackedArgs* p, bool tc) {
+  constexpr long long kSms = 148, kWant = 8 * kSms, kLeast = 256, kMost = 256ll << 20;
+  p->piece_keys = p->max_pieces = 0;
+  const int rows = tc ? 256 : 64;
+  const long long per_seq = ((long long)p->total_q * p->group / p->nseq + rows) / rows;  // row tiles, about
+  const long long tiles = per_seq * p->nseq * p->hk;
+  if (tiles >= 4 * kSms) return;
+  long long keys = (long long)p->total_k * p->hk * per_seq / kWant;
+  if (keys < kLeast) keys = kLeast;
+  keys = (keys + 127) / 128 * 128;
+  const long long row_bytes = (long long)p->total_q * p->hq * (p->d + 1) * 4;
+  while (keys < p->total_k && (p->total_k + keys - 1) / keys * row_bytes > kMost) keys *= 2;
+  if (keys >= p->total_k / p->nseq) return;
+  p->piece_keys = (int)keys;
+  p->max_pieces = (int)((p->total_k + keys - 1) / keys);
+}
+
+size_t packed_workspace_bytes(const PackedArgs& p, na_dtype) {
+  PackedArgs c = p;
+  packed_set_pieces(&c, false);
+  const size_t rows = (size_t)c.max_pieces * c.total_q * c.hq;
+  return rows ? up256(rows * c.d * 4) + up256(rows * 4) : 0;
+}
+
+size_t packed_backward_workspace_bytes(const PackedArgs& p) { return up256((size_t)p.total_q * p.hq * 4); }
+
+cudaError_t launch_packed_forward(PackedArgs p, void* workspace, na_dtype dt, cudaStream_t st) {
+  packed_set_pieces(&p, false);
+  if (p.piece_keys) {
+    p.part_o = (float*)workspace;
+    p.part_lse = (float*)((char*)workspace + up256((size_t)p.max_pieces * p.total_q * p.hq * p.d * 4));
+  }
+  cudaError_t e = by_type(dt, [&](auto t) { return forward_t<decltype(t)>(p, st); });
+  if (e == cudaSuccess && p.piece_keys) e = by_type(dt, [&](auto t) { return join_t<decltype(t)>(p, st); });
+  return e;
+}
+
+cudaError_t launch_packed_backward(PackedArgs p, void* workspace, na_dtype dt, cudaStream_t st) {
+  p.delta = (float*)workspace;
+  if (p.total_q > 0) {
+    cudaError_t e = by_type(dt, [&](auto t) { return delta_t<decltype(t)>(p, st); });
+    if (e != cudaSuccess) return e;
+  }
+  return by_type(dt, [&](auto t) { return backward_t<decltype(t)>(p, st); });
+}
+
+}  // namespace na2d

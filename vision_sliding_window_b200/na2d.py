@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -27,6 +28,9 @@ EXPORTS = (
     "na2d_device_status", "na2d_debug_timeout_probe", "na_status_str",
     "na2d_backward_workspace_bytes", "na2d_backward", "na2d_sasa_workspace_bytes", "na2d_sasa_forward",
     "na2d_block_workspace_bytes", "na2d_block_forward", "na_forward_nd",
+    "na_packed_workspace_bytes", "na_packed_forward", "na_packed_backward_workspace_bytes", "na_packed_backward",
+    "na_norm_forward", "na_norm_backward_workspace_bytes", "na_norm_backward",
+    "na2d_layer_workspace_bytes", "na2d_layer_forward",
 )
 
 
@@ -71,6 +75,22 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.na2d_block_workspace_bytes.restype = sz
         lib.na2d_block_forward.argtypes = [vp] * 8 + [sz, *shape, i, vp]
         lib.na_forward_nd.argtypes = [vp] * 5 + [i] * 12 + [i, vp]
+        ll = ctypes.c_longlong
+        packed = [i] * 6
+        lib.na_packed_workspace_bytes.argtypes = [*packed, i]
+        lib.na_packed_workspace_bytes.restype = sz
+        lib.na_packed_forward.argtypes = [vp] * 9 + [sz, *packed, i, i, f, i, vp]
+        lib.na_packed_backward_workspace_bytes.argtypes = [*packed, i]
+        lib.na_packed_backward_workspace_bytes.restype = sz
+        lib.na_packed_backward.argtypes = [vp] * 12 + [sz, *packed, i, i, f, i, vp]
+        norm = [ll, i, ll, i, i, f, f, i, vp]
+        lib.na_norm_forward.argtypes = [vp] * 9 + norm
+        lib.na_norm_backward_workspace_bytes.argtypes = [ll, i, ll, i]
+        lib.na_norm_backward_workspace_bytes.restype = sz
+        lib.na_norm_backward.argtypes = [vp] * 16 + [sz] + norm
+        lib.na2d_layer_workspace_bytes.argtypes = [*shape, i]
+        lib.na2d_layer_workspace_bytes.restype = sz
+        lib.na2d_layer_forward.argtypes = [vp] * 13 + [sz, *shape, i, i, i, f, f, i, vp]
         lib.na2d_device_status.argtypes = [vp]
         lib.na2d_debug_timeout_probe.argtypes = [ctypes.c_uint, vp]
         lib.na_status_str.argtypes = [i]
@@ -78,7 +98,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         for name in ("na2d_qk_rpb", "na2d_softmax", "na2d_av", "na2d_forward",
                      "na2d_forward_host", "na2d_forward_host_noalloc", "na2d_forward_kernel", "na2d_device_status",
                      "na2d_debug_timeout_probe", "na2d_backward", "na2d_sasa_forward", "na2d_block_forward",
-                     "na_forward_nd"):
+                     "na_forward_nd", "na_packed_forward", "na_packed_backward", "na_norm_forward",
+                     "na_norm_backward", "na2d_layer_forward"):
             getattr(lib, name).restype = i
         _lib = lib
         return lib
@@ -263,6 +284,221 @@ def forward_nd(q, k, v, rpb, ks, dilation=None, out=None):
     _check(load_library().na_forward_nd(_ptr(q), _ptr(k), _ptr(v), _ptr(rpb), _ptr(out), B, heads, *L, d, *kk, *dl,
                                         _DT[q.dtype], _stream(q)), "na_forward_nd")
     return out
+
+
+def _need_all(like, dtype, **tensors):
+    """_need for every tensor that is given, and that it lies on the device of `like`."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        _need(t, name, dtype)
+        if t.device != like.device:
+            raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+
+
+def _need_shape(t, name, shape):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _workspace(given, need: int, like):
+    """The caller's workspace, or one from torch's allocator (None where none is needed)."""
+    if given is None:
+        return (torch.empty(need, dtype=torch.uint8, device=like.device), need) if need else (None, 0)
+    _need_all(like, None, workspace=given)
+    return given, given.numel() * given.element_size()
+
+
+def _packed_dims(q, k, v, cu_q, cu_k, len_k):
+    _need(q, "q")
+    if q.dtype not in _DT:
+        raise ValueError(f"q must be float32, float16 or bfloat16, got {q.dtype}")
+    _need_all(q, q.dtype, k=k, v=v)
+    _need_all(q, torch.int32, cu_q=cu_q, cu_k=cu_k, len_k=len_k)
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q, k and v must be [tokens, heads, d]")
+    _need_shape(v, "v", k.shape)
+    if cu_q.dim() != 1 or cu_q.numel() < 1:
+        raise ValueError("cu_q must be [nseq + 1]")
+    nseq = cu_q.numel() - 1
+    _need_shape(cu_k, "cu_k", (nseq + 1,))
+    _need_shape(len_k, "len_k", (nseq,))
+    if k.shape[2] != q.shape[2]:
+        raise ValueError(f"k and v must have q's head size {q.shape[2]}, got {k.shape[2]}")
+    return nseq, int(q.shape[0]), int(k.shape[0]), int(q.shape[1]), int(k.shape[1]), int(q.shape[2])
+
+
+def packed_forward(q, k, v, cu_q, cu_k, len_k=None, causal: bool = False, window: int = 0, scale=None, out=None,
+                   lse=None, workspace=None):
+    """Attention over packed sequences (na_packed_forward): returns out
+    [total_q, heads_q, d] and lse, float32 [heads_q, total_q].
+
+    q [total_q, heads_q, d]; k, v [total_k, heads_k, d]; sequence s owns the
+    rows cu_q[s]:cu_q[s+1] and the key slots cu_k[s]:cu_k[s+1] (int32, on the
+    device), of which len_k[s] are filled (None: all).  Causal rows stand at
+    the end of their keys and see the last `window` of them (0: all).  scale
+    defaults to d ** -0.5.  Rows of no sequence are not written: what a tensor
+    that this call allocates holds there is not defined."""
+    dims = _packed_dims(q, k, v, cu_q, cu_k, len_k)
+    nseq, tq, _, hq, _, d = dims
+    out = torch.empty_like(q) if out is None else out
+    lse = torch.empty((hq, tq), device=q.device, dtype=torch.float32) if lse is None else lse
+    _need_all(q, q.dtype, out=out)
+    _need_all(q, torch.float32, lse=lse)
+    _need_shape(out, "out", q.shape)
+    _need_shape(lse, "lse", (hq, tq))
+    lib, dt = load_library(), _DT[q.dtype]
+    with torch.cuda.device(q.device):
+        workspace, size = _workspace(workspace, int(lib.na_packed_workspace_bytes(*dims, dt)), q)
+        _check(lib.na_packed_forward(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_q), _ptr(cu_k), _ptr(len_k), _ptr(out),
+                                     _ptr(lse), _ptr(workspace), size, *dims, int(causal), int(window),
+                                     d ** -0.5 if scale is None else float(scale), dt, _stream(q)),
+               "na_packed_forward")
+    return out, lse
+
+
+def packed_backward(q, k, v, out, lse, dout, cu_q, cu_k, causal: bool = False, window: int = 0, scale=None,
+                    grads=None, workspace=None):
+    """Gradients through packed_forward (na_packed_backward): returns (dq, dk,
+    dv), written into `grads` where given.  out and lse are the forward's;
+    rows of no sequence are not written."""
+    dims = _packed_dims(q, k, v, cu_q, cu_k, None)
+    nseq, tq, _, hq, _, d = dims
+    _need_all(q, q.dtype, out=out, dout=dout)
+    _need_all(q, torch.float32, lse=lse)
+    _need_shape(out, "out", q.shape)
+    _need_shape(dout, "dout", q.shape)
+    _need_shape(lse, "lse", (hq, tq))
+    dq, dk, dv = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)) if grads is None else grads
+    _need_all(q, q.dtype, dq=dq, dk=dk, dv=dv)
+    _need_shape(dq, "dq", q.shape)
+    _need_shape(dk, "dk", k.shape)
+    _need_shape(dv, "dv", v.shape)
+    lib, dt = load_library(), _DT[q.dtype]
+    with torch.cuda.device(q.device):
+        workspace, size = _workspace(workspace, int(lib.na_packed_backward_workspace_bytes(*dims, dt)), q)
+        _check(lib.na_packed_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout), _ptr(cu_q),
+                                      _ptr(cu_k), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), size, *dims,
+                                      int(causal), int(window), d ** -0.5 if scale is None else float(scale), dt,
+                                      _stream(q)), "na_packed_backward")
+    return dq, dk, dv
+
+
+def _norm_dims(x, o, post, post_w, post_b, gate, w, b):
+    """rows, C and gates of a norm's tensors; x is [..., C]."""
+    _need(x, "x")
+    if x.dtype not in _DT:
+        raise ValueError(f"x must be float32, float16 or bfloat16, got {x.dtype}")
+    if x.dim() < 1:
+        raise ValueError("x must be [..., C]")
+    _need_all(x, x.dtype, o=o, post_w=post_w, post_b=post_b, gate=gate, w=w, b=b)
+    C = int(x.shape[-1])
+    _need_shape(o, "o", x.shape)
+    for t, n in ((post_w, "post_w"), (post_b, "post_b"), (w, "w"), (b, "b")):
+        _need_shape(t, n, (C,))
+    if gate is not None and (gate.dim() not in (1, 2) or gate.shape[-1] != C):
+        raise ValueError("gate must be [C] or [gates, C]")
+    if o is None and (post or gate is not None):
+        raise ValueError("post and gate act on o, which is missing")
+    if not post and (post_w is not None or post_b is not None):
+        raise ValueError("post_w and post_b need post=True")
+    gates = 0 if gate is None else int(gate.numel() // C) if C else 0
+    return (int(x.numel() // C) if C else 0), C, gates
+
+
+def norm_forward(x, w=None, b=None, o=None, post: bool = False, post_w=None, post_b=None, gate=None,
+                 scale: float = 1.0, eps: float = 1e-5, rms: bool = False, y=None, h=None, norm: bool = True):
+    """The norms around a block with its gate and residual (na_norm_forward):
+    returns (y, h), y = x + scale * gate . P(o) and h = N(y) w + b.
+
+    x, o, y, h [..., C]; N a LayerNorm, or an RMS norm with rms=True; P the
+    same norm with post_w and post_b if post, else the identity.  gate [C] or
+    [gates, C] (each row for an equal share of consecutive rows) or None.
+    o=None: y is x itself.  norm=False: only y, and h is None."""
+    rows, C, gates = _norm_dims(x, o, post, post_w, post_b, gate, w, b)
+    if not norm and (w is not None or b is not None or h is not None or o is None):
+        raise ValueError("norm=False takes o, and neither w, b nor h")
+    if o is None and y is not None:
+        raise ValueError("without o, y is x: there is none to write")
+    if o is not None:
+        y = torch.empty_like(x) if y is None else y
+    if norm:
+        h = torch.empty_like(x) if h is None else h
+    _need_all(x, x.dtype, y=y, h=h)
+    _need_shape(y, "y", x.shape)
+    _need_shape(h, "h", x.shape)
+    with torch.cuda.device(x.device):
+        _check(load_library().na_norm_forward(_ptr(x), _ptr(o), _ptr(post_w), _ptr(post_b), _ptr(gate), _ptr(w),
+                                              _ptr(b), _ptr(y), _ptr(h), rows, C, gates, int(rms), int(post),
+                                              float(eps), float(scale), _DT[x.dtype], _stream(x)),
+               "na_norm_forward")
+    return (x if o is None else y), h
+
+
+class NormGrads(NamedTuple):
+    """What norm_backward returns; None where the input was not given."""
+    dx: torch.Tensor
+    do: torch.Tensor | None
+    dw: torch.Tensor | None
+    db: torch.Tensor | None
+    dpost_w: torch.Tensor | None
+    dpost_b: torch.Tensor | None
+    dgate: torch.Tensor | None
+
+
+def norm_backward(y, dh, dy=None, w=None, b=None, o=None, post: bool = False, post_w=None, post_b=None, gate=None,
+                  scale: float = 1.0, eps: float = 1e-5, rms: bool = False, workspace=None) -> NormGrads:
+    """Gradients through norm_forward (na_norm_backward), y its first result and
+    dh, dy the gradients of both (None: zero).  dx and do have x's type, the
+    others are float32 (dgate of gate's shape)."""
+    rows, C, gates = _norm_dims(y, o, post, post_w, post_b, gate, w, b)
+    if dh is None and (dy is None or w is not None or b is not None):
+        raise ValueError("dh is missing: give dy instead, without w and b")
+    _need_all(y, y.dtype, dh=dh, dy=dy)
+    _need_shape(dh, "dh", y.shape)
+    _need_shape(dy, "dy", y.shape)
+
+    def like(t, dtype=torch.float32):
+        return None if t is None else torch.empty(t.shape, device=y.device, dtype=dtype)
+
+    g = NormGrads(torch.empty_like(y), like(o, y.dtype), like(w), like(b), like(post_w), like(post_b), like(gate))
+    lib, dt = load_library(), _DT[y.dtype]
+    with torch.cuda.device(y.device):
+        workspace, size = _workspace(workspace, int(lib.na_norm_backward_workspace_bytes(rows, C, gates, dt)), y)
+        _check(lib.na_norm_backward(_ptr(y), _ptr(o), _ptr(post_w), _ptr(post_b), _ptr(gate), _ptr(w), _ptr(dy),
+                                    _ptr(dh), _ptr(g.dx), _ptr(g.do), _ptr(g.dw), _ptr(g.db), _ptr(g.dpost_w),
+                                    _ptr(g.dpost_b), _ptr(g.dgate), _ptr(workspace), size, rows, C, gates, int(rms),
+                                    int(post), float(eps), float(scale), dt, _stream(y)), "na_norm_backward")
+    return g
+
+
+def layer_forward(x, w, b, wqkv, bqkv, wo, bo, rpb, heads: int, ksize: int, gate=None, post: bool = False,
+                  post_w=None, post_b=None, scale: float = 1.0, eps: float = 1e-5, rms: bool = False, y=None,
+                  workspace=None):
+    """The attention half of a NAT layer (na2d_layer_forward): returns
+    x + scale * gate . P(block(N(x) w + b)), x [B, H, W, heads * dh]; the block's
+    arguments as in block_forward, the norms' as in norm_forward."""
+    if x.dim() != 4:
+        raise ValueError("x must be [B, H, W, C]")
+    _, C, gates = _norm_dims(x, x, post, post_w, post_b, gate, w, b)
+    _need_all(x, x.dtype, wqkv=wqkv, bqkv=bqkv, wo=wo, bo=bo, rpb=rpb)
+    if heads < 1 or C % heads:
+        raise ValueError("C must be a multiple of heads")
+    B, H, W = (int(n) for n in x.shape[:3])
+    for t, n, shape in ((wqkv, "wqkv", (C, 3 * C)), (bqkv, "bqkv", (3 * C,)), (wo, "wo", (C, C)), (bo, "bo", (C,)),
+                        (rpb, "rpb", (heads, 2 * ksize - 1, 2 * ksize - 1))):
+        _need_shape(t, n, shape)
+    y = torch.empty_like(x) if y is None else y
+    _need_all(x, x.dtype, y=y)
+    _need_shape(y, "y", x.shape)
+    lib, dt, dims = load_library(), _DT[x.dtype], (B, H, W, heads, C // heads, ksize)
+    with torch.cuda.device(x.device):
+        workspace, size = _workspace(workspace, int(lib.na2d_layer_workspace_bytes(*dims, dt)), x)
+        _check(lib.na2d_layer_forward(_ptr(x), _ptr(w), _ptr(b), _ptr(wqkv), _ptr(bqkv), _ptr(wo), _ptr(bo),
+                                      _ptr(rpb), _ptr(post_w), _ptr(post_b), _ptr(gate), _ptr(y), _ptr(workspace),
+                                      size, *dims, gates, int(rms), int(post), float(eps), float(scale), dt,
+                                      _stream(x)), "na2d_layer_forward")
+    return y
 
 
 def host_workspace_bytes(B, heads, H, W, d, ksize, dtype) -> int:
