@@ -84,15 +84,19 @@ struct PackedArgs {
   void *dq, *dk, *dv;
   int nseq, total_q, total_k, hq, hk, group, d, causal, window;
   float scale;
-  // keys of a piece when a sequence's keys are cut into pieces that are
-  // joined afterwards (0: not cut), and the pieces' results
-  int piece_keys, max_pieces;
+  // Sequences' keys are cut into at most max_pieces pieces that are joined
+  // afterwards (1: not cut), of piece_keys keys each, or (0) the same number of
+  // pieces for every sequence; and the pieces' results
+  int path, piece_keys, max_pieces;
   float *part_o, *part_lse;  // [max_pieces][total_q][hq][d] and [max_pieces][total_q][hq]
   float* delta;              // backward: [total_q][hq]
   unsigned* status;
 };
-// Sets piece_keys and max_pieces, from sizes alone (na_packed_simt.cu).
-void packed_set_pieces(PackedArgs* p, bool tc);
+enum { kPathSimt, kPathRows, kPathTc };
+// Sets path, piece_keys and max_pieces (na_packed_simt.cu).
+void packed_plan(PackedArgs* p, na_dtype dt);
+cudaError_t launch_packed_forward_rows(const PackedArgs& p, na_dtype dt, cudaStream_t st);  // na_packed_rows.cu
+cudaError_t launch_packed_forward_tc(const PackedArgs& p, na_dtype dt, cudaStream_t st);    // na_packed_tc.cu
 size_t packed_workspace_bytes(const PackedArgs& p, na_dtype dt);
 size_t packed_backward_workspace_bytes(const PackedArgs& p);
 cudaError_t launch_packed_forward(PackedArgs p, void* workspace, na_dtype dt, cudaStream_t st);

@@ -58,6 +58,13 @@ NA_DEVICE void seen_by(const PackedArgs& p, const Span& s, int j, int* lo, int* 
   }
 }
 
+// Keys of a piece of a sequence whose keys are cut: fixed, or its share when
+// every sequence is cut into the same number of pieces.
+NA_DEVICE int piece_length(const PackedArgs& p, const Span& s) {
+  if (p.piece_keys > 0) return p.piece_keys;
+  return max((s.nk + p.max_pieces * 128 - 1) / (p.max_pieces * 128), 1) * 128;
+}
+
 // Parts of `per` consecutive units of the sequences' entries, `mul` units an
 // entry, are numbered without counting them: sequence s owns the numbers from
 // cu[s] mul / per + s on, which are enough for its ceil(n mul / per) parts, as
@@ -82,6 +89,109 @@ NA_DEVICE void find_part(const int* cu, int nseq, int total, int mul, int per, l
   }
   *s = a;
   *idx = number - first_number(cu, a, total, mul, per);
+}
+
+// find_part by a whole warp: 32 probes at once, so that one round of loads
+// finds the sequence among 32 and two among 1024.
+NA_DEVICE void find_part_warp(const int* cu, int nseq, int total, int mul, int per, long long number, int* s,
+                              long long* idx) {
+  const int lane = threadIdx.x & 31;
+  int a = 0, n = nseq;  // the answer is one of a .. a + n - 1
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int at = a + lane * step;
+    const bool below = lane * step < n && first_number(cu, at, total, mul, per) <= number;
+    const unsigned votes = __ballot_sync(0xffffffffu, below) | 1u;
+    const int last = 31 - __clz(votes);
+    const int end = a + n;
+    a += last * step;
+    n = min(step, end - a);
+  }
+  *s = a;
+  *idx = number - first_number(cu, a, total, mul, per);
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <typename T> NA_DEVICE float to_f(T x);
+template <> NA_DEVICE float to_f<float>(float x) { return x; }
+template <> NA_DEVICE float to_f<__half>(__half x) { return __half2float(x); }
+template <> NA_DEVICE float to_f<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T> NA_DEVICE T from_f(float x);
+template <> NA_DEVICE float from_f<float>(float x) { return x; }
+template <> NA_DEVICE __half from_f<__half>(float x) { return __float2half_rn(x); }
+template <> NA_DEVICE __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// two values rounded and packed, a in the low half
+template <typename T> NA_DEVICE uint32_t pack2(float a, float b) {
+  uint32_t r;
+  if constexpr (sizeof(T) == 2) {
+    if constexpr (__is_same(T, __half))
+      asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    else
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  }
+  return r;
+}
+
+NA_DEVICE float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+NA_DEVICE float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+
+// a . b of D elements
+template <typename T, int D> NA_DEVICE float dot_row(const T* a, const T* b) {
+  constexpr int VEC = 16 / sizeof(T);
+  float s = 0.f;
+  for (int i = 0; i < D; i += VEC) {
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(a + i)), y = __ldg(reinterpret_cast<const uint4*>(b + i));
+    const T *u = reinterpret_cast<const T*>(&x), *v = reinterpret_cast<const T*>(&y);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) s = fmaf(to_f<T>(u[e]), to_f<T>(v[e]), s);
+  }
+  return s;
+}
+
+// One row over its keys [lo, hi) by a whole warp, from global memory: every
+// key outside is left out of the sums, not multiplied by zero.  Matrix
+// instructions cannot leave out single entries, so a row whose result is not
+// finite is taken again by this.  acc holds the columns lane + 32 e, not yet
+// divided by *sum; logits are in units of log2 with *top as their reference.
+template <typename T, int D>
+NA_DEVICE void exact_row(const PackedArgs& p, const T* q, const T* k, const T* v, long long stride, int lo, int hi,
+                         float (&acc)[(D + 31) / 32], float* sum, float* top) {
+  const int lane = threadIdx.x & 31;
+  const float sl2 = p.scale * kLog2e;
+  float m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int e = 0; e < (D + 31) / 32; ++e) acc[e] = 0.f;
+  for (int j0 = lo; j0 < hi; j0 += 32) {
+    const bool live = j0 + lane < hi;
+    const float s = live ? dot_row<T, D>(q, k + (j0 + lane) * stride) * sl2 : -INFINITY;
+    const float mx = fmaxf(m, warp_max(s));
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    const float f = exp2f(m - ref);
+    const float e = live ? exp2f(s - ref) : 0.f;
+    l = fmaf(l, f, warp_sum(e));
+    m = mx;
+#pragma unroll
+    for (int c = 0; c < (D + 31) / 32; ++c) acc[c] *= f;
+    for (int t = 0; t < min(32, hi - j0); ++t) {
+      const float w = __shfl_sync(0xffffffffu, e, t);
+#pragma unroll
+      for (int c = 0; c < (D + 31) / 32; ++c)
+        if (lane + 32 * c < D) acc[c] = fmaf(w, to_f<T>(v[(j0 + t) * stride + lane + 32 * c]), acc[c]);
+    }
+  }
+  *sum = l;
+  *top = m == -INFINITY ? 0.f : m;
 }
 
 }  // namespace packed

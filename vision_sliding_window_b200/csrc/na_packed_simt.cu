@@ -26,19 +26,8 @@ namespace {
 
 using namespace packed;
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kKeys = 64;  // keys of a tile
 constexpr int kThreads = 128;
-
-template <typename T> NA_DEVICE float to_f(T x);
-template <> NA_DEVICE float to_f<float>(float x) { return x; }
-template <> NA_DEVICE float to_f<__half>(__half x) { return __half2float(x); }
-template <> NA_DEVICE float to_f<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <typename T> NA_DEVICE T from_f(float x);
-template <> NA_DEVICE float from_f<float>(float x) { return x; }
-template <> NA_DEVICE __half from_f<__half>(float x) { return __float2half_rn(x); }
-template <> NA_DEVICE __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
 // Loads `n` vectors' worth of a row of D elements into shared float32.
 template <typename T, int D> NA_DEVICE void load_vec(const T* g, float* s, int v, bool live) {
@@ -296,7 +285,8 @@ __global__ void __launch_bounds__(256) packed_join_kernel(PackedArgs p) {
   if (i < sp.q0 || i >= sp.q0 + sp.nq) return;
   int lo, hi;
   visible(p, sp, i - sp.q0, &lo, &hi);
-  const int c0 = lo / p.piece_keys, c1 = lo < hi ? min((hi - 1) / p.piece_keys + 1, p.max_pieces) : c0;
+  const int len = piece_length(p, sp);
+  const int c0 = lo / len, c1 = lo < hi ? min((hi - 1) / len + 1, p.max_pieces) : c0;
   const long long step = (long long)p.total_q * p.hq;
   float mx = -INFINITY;
   for (int c = c0 + lane; c < c1; c += 32) mx = fmaxf(mx, p.part_lse[c * step + row]);
@@ -588,45 +578,68 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
-// The keys are cut when the row tiles alone leave SMs idle: single tokens,
-// and short prompts over long caches.  Pieces are as long as leaves about
-// kWant blocks, not under kLeast keys (each piece's rows pay for writing and
-// joining a float32 output), and a cut pays only where a sequence of average
-// length spans several.
-void packed_set_pieces(PackedArgs* p, bool tc) {
-  constexpr long long kSms = 148, kWant = 8 * kSms, kLeast = 256, kMost = 256ll << 20;
-  p->piece_keys = p->max_pieces = 0;
-  const int rows = tc ? 256 : 64;
-  const long long per_seq = ((long long)p->total_q * p->group / p->nseq + rows) / rows;  // row tiles, about
-  const long long tiles = per_seq * p->nseq * p->hk;
-  if (tiles >= 4 * kSms) return;
-  long long keys = (long long)p->total_k * p->hk * per_seq / kWant;
-  if (keys < kLeast) keys = kLeast;
-  keys = (keys + 127) / 128 * 128;
+// Which kernel runs a forward call, and how it cuts the keys, from sizes and
+// type alone.
+//
+// Few rows a sequence (16 on average: single tokens of up to 16 heads a group)
+// run a block for each piece of keys; float32, groups wider than a row tile
+// and calls without keys run on the CUDA cores; the rest on the tensor cores.
+//
+// A cut of the keys pays where the row tiles alone leave SMs idle.  Kernels
+// that own a few rows cut every sequence into pieces of one length, as long as
+// leaves about `want` blocks but not under 256 keys (each piece's rows pay for
+// writing and joining a float32 output), so that long sequences make more
+// pieces than short ones.  The tensor-core kernel cuts every sequence into the
+// same number of pieces of 512 keys at least, as its grid counts row tiles.
+void packed_plan(PackedArgs* p, na_dtype dt) {
+  constexpr long long kSms = 148, kMost = 256ll << 20;
+  p->piece_keys = 0;
+  p->max_pieces = 1;
+  const bool few = (long long)p->total_q * p->group <= 16ll * p->nseq;
+  p->path = dt == NA_F32 || p->group > 128 || p->total_k == 0 ? kPathSimt : few ? kPathRows : kPathTc;
   const long long row_bytes = (long long)p->total_q * p->hq * (p->d + 1) * 4;
+  if (p->path == kPathTc) {
+    const int per = 2 * (128 / p->group);
+    const long long tiles = part_numbers(p->nseq, p->total_q, 1, per) * p->hk;
+    long long pieces = kSms / tiles;
+    if (pieces > p->total_k / p->nseq / 512) pieces = p->total_k / p->nseq / 512;
+    while (pieces > 1 && pieces * row_bytes > kMost) --pieces;
+    if (pieces > 1) p->max_pieces = (int)pieces;
+    return;
+  }
+  const int rows = few ? 16 : 64;
+  const long long want = (p->path == kPathRows ? 16 : 8) * kSms, least = 256;
+  const long long per_seq = ((long long)p->total_q * p->group / p->nseq + rows) / rows;  // row tiles, about
+  if (per_seq * p->nseq * p->hk >= 4 * kSms) return;
+  long long keys = (long long)p->total_k * p->hk * per_seq / want;
+  if (keys < least) keys = least;
+  keys = (keys + 127) / 128 * 128;
   while (keys < p->total_k && (p->total_k + keys - 1) / keys * row_bytes > kMost) keys *= 2;
-  if (keys >= p->total_k / p->nseq) return;
+  if (p->total_k == 0 || keys >= p->total_k / p->nseq) return;
   p->piece_keys = (int)keys;
   p->max_pieces = (int)((p->total_k + keys - 1) / keys);
 }
 
-size_t packed_workspace_bytes(const PackedArgs& p, na_dtype) {
+size_t packed_workspace_bytes(const PackedArgs& p, na_dtype dt) {
   PackedArgs c = p;
-  packed_set_pieces(&c, false);
+  packed_plan(&c, dt);
+  if (c.max_pieces < 2) return 0;
   const size_t rows = (size_t)c.max_pieces * c.total_q * c.hq;
-  return rows ? up256(rows * c.d * 4) + up256(rows * 4) : 0;
+  return up256(rows * c.d * 4) + up256(rows * 4);
 }
 
 size_t packed_backward_workspace_bytes(const PackedArgs& p) { return up256((size_t)p.total_q * p.hq * 4); }
 
 cudaError_t launch_packed_forward(PackedArgs p, void* workspace, na_dtype dt, cudaStream_t st) {
-  packed_set_pieces(&p, false);
-  if (p.piece_keys) {
+  packed_plan(&p, dt);
+  if (p.max_pieces > 1) {
     p.part_o = (float*)workspace;
     p.part_lse = (float*)((char*)workspace + up256((size_t)p.max_pieces * p.total_q * p.hq * p.d * 4));
   }
-  cudaError_t e = by_type(dt, [&](auto t) { return forward_t<decltype(t)>(p, st); });
-  if (e == cudaSuccess && p.piece_keys) e = by_type(dt, [&](auto t) { return join_t<decltype(t)>(p, st); });
+  cudaError_t e = p.path == kPathTc     ? launch_packed_forward_tc(p, dt, st)
+                  : p.path == kPathRows ? launch_packed_forward_rows(p, dt, st)
+                                        : by_type(dt, [&](auto t) { return forward_t<decltype(t)>(p, st); });
+  if (e == cudaSuccess && p.max_pieces > 1) e = by_type(dt, [&](auto t) { return join_t<decltype(t)>(p, st); });
   return e;
 }
 
