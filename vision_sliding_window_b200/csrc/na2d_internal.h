@@ -88,8 +88,9 @@ struct PackedArgs {
   // afterwards (1: not cut), of piece_keys keys each, or (0) the same number of
   // pieces for every sequence; and the pieces' results
   int path, piece_keys, max_pieces;
-  float *part_o, *part_lse;  // [max_pieces][total_q][hq][d] and [max_pieces][total_q][hq]
-  float* delta;              // backward: [total_q][hq]
+  float *part_o, *part_lse;  // [max_pieces][total_q][hq][d] and [max_pieces][total_q][hq];
+                             // backward: [max_pieces][2][total_k][hk][d], dv and dk
+  float2* terms;  // backward: (lse log2 e, out . dout) of every row, [total_q][hq]
   unsigned* status;
 };
 enum { kPathSimt, kPathRows, kPathTc };
@@ -97,8 +98,10 @@ enum { kPathSimt, kPathRows, kPathTc };
 void packed_plan(PackedArgs* p, na_dtype dt);
 cudaError_t launch_packed_forward_rows(const PackedArgs& p, na_dtype dt, cudaStream_t st);  // na_packed_rows.cu
 cudaError_t launch_packed_forward_tc(const PackedArgs& p, na_dtype dt, cudaStream_t st);    // na_packed_tc.cu
+void packed_backward_plan(PackedArgs* p, na_dtype dt);  // sets path and max_pieces
+cudaError_t launch_packed_backward_tc(const PackedArgs& p, na_dtype dt, cudaStream_t st);   // na_packed_tc_bwd.cu
 size_t packed_workspace_bytes(const PackedArgs& p, na_dtype dt);
-size_t packed_backward_workspace_bytes(const PackedArgs& p);
+size_t packed_backward_workspace_bytes(const PackedArgs& p, na_dtype dt);
 cudaError_t launch_packed_forward(PackedArgs p, void* workspace, na_dtype dt, cudaStream_t st);
 cudaError_t launch_packed_backward(PackedArgs p, void* workspace, na_dtype dt, cudaStream_t st);
 

@@ -112,7 +112,7 @@ NA_EXPORT size_t na_packed_backward_workspace_bytes(int nseq, int total_q, int t
   PackedArgs p;
   if (check_packed(nseq, total_q, total_k, heads_q, heads_k, d, 0, 0, 1.f, dt, &p) != NA_OK) return 0;
   if (nseq == 0 || total_q == 0) return 0;
-  return packed_backward_workspace_bytes(p);
+  return packed_backward_workspace_bytes(p, dt);
 }
 
 NA_EXPORT na_status na_packed_backward(const void* q, const void* k, const void* v, const void* out, const float* lse,
@@ -128,7 +128,7 @@ NA_EXPORT na_status na_packed_backward(const void* q, const void* k, const void*
   if (bad(q, rows) || bad(out, rows) || bad(dout, rows) || bad(dq, rows) || bad(lse, rows, 4)) return NA_ERR_INVALID_ARG;
   if (bad(k, keys) || bad(v, keys) || bad(dk, keys) || bad(dv, keys)) return NA_ERR_INVALID_ARG;
   if (bad(cu_q, true, 4) || bad(cu_k, true, 4)) return NA_ERR_INVALID_ARG;
-  const size_t need = rows ? packed_backward_workspace_bytes(p) : 0;
+  const size_t need = rows ? packed_backward_workspace_bytes(p, dt) : 0;
   if (bad(workspace, need > 0, 256) || workspace_bytes < need) return NA_ERR_INVALID_ARG;
   if (status_word(&p.status) != cudaSuccess) return NA_ERR_CUDA;
   p.q = q;

@@ -310,8 +310,8 @@ __global__ void __launch_bounds__(256) packed_join_kernel(PackedArgs p) {
 }
 
 // ---------------------------------------------------------------- backward
-// delta = out . dout for every row, [total_q][hq]
-template <typename T, int D> __global__ void __launch_bounds__(256) packed_delta_kernel(PackedArgs p) {
+// Every row's log-sum-exp in units of log2 and delta = out . dout.
+template <typename T, int D> __global__ void __launch_bounds__(256) packed_terms_kernel(PackedArgs p) {
   constexpr int VEC = 16 / sizeof(T), LPR = D / VEC;  // lanes a row
   const long long row = ((long long)blockIdx.x * 256 + threadIdx.x) / LPR;
   const int v = threadIdx.x % LPR;
@@ -326,7 +326,8 @@ template <typename T, int D> __global__ void __launch_bounds__(256) packed_delta
   }
 #pragma unroll
   for (int o = 1; o < LPR; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (live && v == 0) p.delta[row] = s;
+  if (live && v == 0)
+    p.terms[row] = make_float2(p.lse_in[row % p.hq * p.total_q + row / p.hq] * kLog2e, s);
 }
 
 template <int D> constexpr int bwd_smem() {
@@ -341,8 +342,9 @@ NA_DEVICE void load_row_terms(const PackedArgs& p, const Span& sp, int kh, long 
     const long long rr = r0 + (r < n ? r : 0);
     const long long i = (long long)sp.q0 + rr / p.group;
     const int head = kh * p.group + (int)(rr % p.group);
-    lse[r] = p.lse_in[(long long)head * p.total_q + i] * kLog2e;
-    delta[r] = p.delta[i * p.hq + head];
+    const float2 t = p.terms[i * p.hq + head];
+    lse[r] = t.x;
+    delta[r] = t.y;
   }
 }
 
@@ -543,19 +545,19 @@ template <typename T> cudaError_t backward_t(const PackedArgs& p, cudaStream_t s
   }
   return cudaErrorInvalidValue;
 }
-template <typename T, int D> cudaError_t delta_d(const PackedArgs& p, cudaStream_t st) {
+template <typename T, int D> cudaError_t terms_d(const PackedArgs& p, cudaStream_t st) {
   constexpr int kRows = 256 * 16 / ((int)sizeof(T) * D);
   const long long rows = (long long)p.total_q * p.hq, blocks = (rows + kRows - 1) / kRows;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  packed_delta_kernel<T, D><<<(unsigned)blocks, 256, 0, st>>>(p);
+  packed_terms_kernel<T, D><<<(unsigned)blocks, 256, 0, st>>>(p);
   return cudaGetLastError();
 }
-template <typename T> cudaError_t delta_t(const PackedArgs& p, cudaStream_t st) {
+template <typename T> cudaError_t terms_t(const PackedArgs& p, cudaStream_t st) {
   switch (p.d) {
-    case 16: return delta_d<T, 16>(p, st);
-    case 32: return delta_d<T, 32>(p, st);
-    case 64: return delta_d<T, 64>(p, st);
-    case 128: return delta_d<T, 128>(p, st);
+    case 16: return terms_d<T, 16>(p, st);
+    case 32: return terms_d<T, 32>(p, st);
+    case 64: return terms_d<T, 64>(p, st);
+    case 128: return terms_d<T, 128>(p, st);
   }
   return cudaErrorInvalidValue;
 }
@@ -628,7 +630,31 @@ size_t packed_workspace_bytes(const PackedArgs& p, na_dtype dt) {
   return up256(rows * c.d * 4) + up256(rows * 4);
 }
 
-size_t packed_backward_workspace_bytes(const PackedArgs& p) { return up256((size_t)p.total_q * p.hq * 4); }
+// The backward's kernels, chosen as the forward's.  The key tiles' walks over
+// rows are cut into pieces, whose sums are added afterwards, where the key
+// tiles alone are fewer than about 5 blocks for 2 SMs: causal walks have
+// unequal lengths and the longest would run alone.
+void packed_backward_plan(PackedArgs* p, na_dtype dt) {
+  constexpr long long kSms = 148, kMost = 512ll << 20;
+  p->piece_keys = 0;
+  p->max_pieces = 1;
+  p->path = dt == NA_F32 || p->group > 128 || p->total_k == 0 || p->total_q == 0 ? kPathSimt : kPathTc;
+  if (p->path != kPathTc) return;
+  const long long tiles = part_numbers(p->nseq, p->total_k, 1, 128) * p->hk;
+  const long long walk = (long long)p->total_q / p->nseq / (128 / p->group);  // row tiles of a key tile, about
+  long long pieces = (5 * kSms / 2 + tiles - 1) / tiles;
+  if (pieces > walk / 8) pieces = walk / 8;
+  if (pieces > 8) pieces = 8;
+  while (pieces > 1 && pieces * p->total_k * p->hk * p->d * 8 > kMost) --pieces;
+  if (pieces > 1) p->max_pieces = (int)pieces;
+}
+
+size_t packed_backward_workspace_bytes(const PackedArgs& p, na_dtype dt) {
+  PackedArgs c = p;
+  packed_backward_plan(&c, dt);
+  const size_t sums = c.max_pieces > 1 ? (size_t)c.max_pieces * c.total_k * c.hk * c.d * 8 : 0;
+  return up256((size_t)p.total_q * p.hq * 8) + up256(sums);
+}
 
 cudaError_t launch_packed_forward(PackedArgs p, void* workspace, na_dtype dt, cudaStream_t st) {
   packed_plan(&p, dt);
@@ -644,11 +670,14 @@ cudaError_t launch_packed_forward(PackedArgs p, void* workspace, na_dtype dt, cu
 }
 
 cudaError_t launch_packed_backward(PackedArgs p, void* workspace, na_dtype dt, cudaStream_t st) {
-  p.delta = (float*)workspace;
+  packed_backward_plan(&p, dt);
+  p.terms = (float2*)workspace;
+  p.part_o = (float*)((char*)workspace + up256((size_t)p.total_q * p.hq * 8));
   if (p.total_q > 0) {
-    cudaError_t e = by_type(dt, [&](auto t) { return delta_t<decltype(t)>(p, st); });
+    cudaError_t e = by_type(dt, [&](auto t) { return terms_t<decltype(t)>(p, st); });
     if (e != cudaSuccess) return e;
   }
+  if (p.path == kPathTc) return launch_packed_backward_tc(p, dt, st);
   return by_type(dt, [&](auto t) { return backward_t<decltype(t)>(p, st); });
 }
 

@@ -60,6 +60,14 @@ template <int D, bool BF16> NA_DEVICE void mma_weights_by_tile(uint32_t d, uint3
   for (int kk = 0; kk < kTile / 16; ++kk) mma_ts(d, a + kk * 8, mn_major<D>(b, kk), idesc, (add || kk > 0) ? 1u : 0u);
 }
 
+// The same with the operand's two halves of 64 in tensor memory 64 columns apart.
+template <int D, bool BF16> NA_DEVICE void mma_halves_by_tile(uint32_t d, uint32_t a, uint32_t b, bool add) {
+  constexpr uint32_t idesc = idesc_f16(BF16, kTile, D, true);
+#pragma unroll
+  for (int kk = 0; kk < kTile / 16; ++kk)
+    mma_ts(d, a + (kk / 4) * 64 + (kk % 4) * 8, mn_major<D>(b, kk), idesc, (add || kk > 0) ? 1u : 0u);
+}
+
 // All column blocks of 128 keys from key `row` on of head kh.
 template <int D> NA_DEVICE void load_key_tile(uint32_t dst, const CUtensorMap* m, uint32_t bar, int kh, int row) {
   using G = Geo<D>;

@@ -1,0 +1,708 @@
+// na_packed_tc_bwd.cu -- gradients of the packed attention on the tensor cores,
+// fp16 and bf16.
+//
+// Two kernels, both of which recompute the weights from the rows' log-sum-exp:
+//
+//   dk, dv   a block owns 128 keys and walks the row tiles that see them:
+//            S^T = K Q^T, dP^T = V dO^T, P^T = 2^(S^T scale log2e - lse),
+//            dS^T = P^T (dP^T - delta), dV += P^T dO, dK += dS^T Q;
+//   dq       a block owns a row tile and walks the keys it sees:
+//            S = Q K^T, dP = dO V^T, dS likewise, dQ += dS K.
+//
+// That is seven products where one kernel that owned keys and added dq to
+// memory with atomics would need five; in exchange each gradient is one
+// block's sum in a fixed order and no float32 copy of dq goes through memory.
+// The heads of a group are rows like any others, so a shared head's gradient
+// needs no further sum.
+//
+// P^T and dS^T are written over S^T and dP^T (16 bits) and read as operands
+// from tensor memory.  The products are issued so that the tensor pipe always
+// has one while a half of the element-wise work runs: dV and the next S^T
+// beside dS^T, dK and the next dP^T beside P^T.  Two warpgroups share a tile,
+// each 64 of its columns, a thread a lane.  Shared-memory reads of the
+// operands bound the first kernel at d = 128 (two products with both operands
+// there and two with one: 1536 of about 2048 cycles of a step, and the
+// copies' writes 512 more).
+//
+// P and dS are rounded to the input type for their products.
+#include "na_packed_tc.cuh"
+
+namespace na2d {
+namespace {
+
+using namespace packed;
+
+template <int D> struct Bwd {
+  using G = Geo<D>;
+  static constexpr int STAGES = D == 128 ? 2 : 4;
+  static constexpr int RING_OFF = 2 * G::TILE_BYTES;  // the two tiles that stay come first
+  static constexpr int TERMS_OFF = RING_OFF + STAGES * 2 * G::TILE_BYTES;
+  static constexpr int BAR_OFF = TERMS_OFF + STAGES * 2 * kTile * 4;
+  static constexpr int SMEM = BAR_OFF + 256 + 1024;
+  static constexpr int SMEM_ASKED = SMEM > 116 * 1024 ? SMEM : 116 * 1024;  // one block an SM: it holds all of tensor memory
+  static_assert(SMEM <= kMaxSmem, "fits");
+  static constexpr int THREADS = 384;
+  static constexpr int REGS_CTRL = 72, REGS_WORK = 216;
+};
+
+struct Bars {
+  uint32_t base;
+  int stages;
+  NA_DEVICE uint32_t kept() const { return base; }
+  NA_DEVICE uint32_t tail() const { return base + 8; }
+  NA_DEVICE uint32_t done() const { return base + 16; }
+  NA_DEVICE uint32_t s() const { return base + 24; }
+  NA_DEVICE uint32_t dp() const { return base + 32; }
+  NA_DEVICE uint32_t p_ready() const { return base + 40; }
+  NA_DEVICE uint32_t ds_ready() const { return base + 48; }
+  NA_DEVICE uint32_t full(int i) const { return base + 56 + (i % stages) * 8; }
+  NA_DEVICE uint32_t empty(int i) const { return base + 56 + (stages + i % stages) * 8; }
+  NA_DEVICE void init(int full_count) const {
+    mbar_init(kept(), 1);
+    mbar_init(tail(), 1);
+    mbar_init(done(), 1);
+    mbar_init(s(), 1);
+    mbar_init(dp(), 1);
+    mbar_init(p_ready(), 8);
+    mbar_init(ds_ready(), 8);
+    for (int i = 0; i < stages; ++i) {
+      mbar_init(full(i), full_count);
+      mbar_init(empty(i), 1);
+    }
+    mbar_init_fence();
+  }
+};
+
+template <int W> NA_DEVICE void tmem_ld_n(uint32_t at, uint32_t (&r)[W]) {
+  if constexpr (W == 32)
+    tmem_ld32(at, r);
+  else if constexpr (W == 16)
+    tmem_ld16(at, r);
+  else
+    tmem_ld8(at, r);
+  tmem_wait_ld_regs(r);
+}
+
+// A store of W consecutive results, in dt or in float32.
+template <typename T, int W> NA_DEVICE void store_run(T* to, const float (&f)[W]) {
+#pragma unroll
+  for (int e = 0; e < W; e += 8)
+    *reinterpret_cast<uint4*>(to + e) = make_uint4(pack2<T>(f[e], f[e + 1]), pack2<T>(f[e + 2], f[e + 3]),
+                                                   pack2<T>(f[e + 4], f[e + 5]), pack2<T>(f[e + 6], f[e + 7]));
+}
+template <int W> NA_DEVICE void store_run(float* to, const float (&f)[W]) {
+#pragma unroll
+  for (int e = 0; e < W; e += 4) *reinterpret_cast<float4*>(to + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+}
+
+// The weight and its gradient of one row and key, from global memory.
+template <typename T, int D>
+NA_DEVICE void exact_pair(const PackedArgs& p, long long row, long long key, float* w, float* ds) {
+  const float2 term = p.terms[row];
+  const float s = dot_row<T, D>((const T*)p.q + row * D, (const T*)p.k + key * D);
+  const float dp = dot_row<T, D>((const T*)p.dout + row * D, (const T*)p.v + key * D);
+  *w = exp2f(fmaf(s, p.scale * kLog2e, -term.x));
+  *ds = *w * (dp - term.y);
+}
+
+// ------------------------------------------------------------------ dk, dv
+template <typename T, int D>
+__global__ void __launch_bounds__(Bwd<D>::THREADS, 1)
+packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mo,
+                      const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                      const PackedArgs p) {
+  using C = Bwd<D>;
+  using G = Geo<D>;
+  constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value;
+  extern __shared__ uint8_t raw[];
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  const int P = kTile / p.group, kh = blockIdx.y, Z = p.max_pieces;
+  int s;
+  long long idx;
+  find_part_warp(p.cu_k, p.nseq, p.total_k, 1, kTile, blockIdx.x, &s, &idx);
+  if (idx < 0) return;
+  const Span sp = span_of(p, s);
+  if (idx * kTile >= sp.nk) return;
+  const int j0 = (int)idx * kTile, nk = min(kTile, sp.nk - j0);
+  // row tiles: positions first + (z + i Z) P, i = 0 .. n - 1
+  int first, last, unused;
+  seen_by(p, sp, j0, &first, &unused);
+  seen_by(p, sp, j0 + nk - 1, &unused, &last);
+  const int tiles = last > first ? (last - first + P - 1) / P : 0, z = blockIdx.z;
+  const int n = tiles > z ? (tiles - z + Z - 1) / Z : 0;
+  auto tile_pos = [&](int i) { return first + (z + i * Z) * P; };
+
+  const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
+  const uint32_t k_tile = base, v_tile = base + G::TILE_BYTES;
+  auto q_tile = [&](int i) { return base + C::RING_OFF + (i % C::STAGES) * 2 * G::TILE_BYTES; };
+  auto o_tile = [&](int i) { return q_tile(i) + G::TILE_BYTES; };
+  float* terms = reinterpret_cast<float*>(raw + (base - smem_addr(raw)) + C::TERMS_OFF);
+  auto lse_of = [&](int i) { return terms + (i % C::STAGES) * 2 * kTile; };
+  const Bars bar{base + C::BAR_OFF, C::STAGES};
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    bar.init(2);  // the copies, and the rows' terms
+  }
+  if (warp == 1) tmem_alloc(smem_addr(&tmem_slot), 512);
+  if (P * p.group < kTile && warp >= 4)  // rows of a tile that no copy fills
+    for (int i = warp - 4; i < 2 * C::STAGES; i += 8) zero_rows<D>(base + C::RING_OFF + i * G::TILE_BYTES, P * p.group);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const uint32_t s_at = tmem, dp_at = tmem + 128, dv_at = tmem + 256, dk_at = tmem + 256 + D;
+  volatile int* ab = &abort_flag;
+
+  if (warp < 4) {
+    regs_dec<C::REGS_CTRL>();
+    if (warp == 0 && n > 0) {
+      // ------------------------------------------------------------- loads
+      if (lane == 0) {
+        mbar_expect_tx(bar.kept(), 2 * G::TILE_BYTES);
+        load_key_tile<D>(k_tile, &mk, bar.kept(), kh, sp.k0 + j0);
+        load_key_tile<D>(v_tile, &mv, bar.kept(), kh, sp.k0 + j0);
+      }
+      const uint32_t bytes = (uint32_t)(2 * P * p.group * D * 2);
+      bool tail_used = false;
+      int i = 0;
+      for (; i < n; ++i) {
+        if (i >= C::STAGES && !mbar_wait(bar.empty(i), ((i / C::STAGES) - 1) & 1, ab, p.status)) break;
+        const int pos = tile_pos(i);
+        // rows past the sequence are zeroed: what they hold may be NaN
+        const bool tail = pos + P > sp.nq;
+        const uint32_t b = tail ? bar.tail() : bar.full(i);
+        if (lane == 0) {
+          mbar_expect_tx(b, bytes);
+          load_row_tile<D>(q_tile(i), &mq, b, kh, sp.q0 + pos);
+          load_row_tile<D>(o_tile(i), &mo, b, kh, sp.q0 + pos);
+        }
+        __syncwarp();
+        if (tail) {
+          tail_used = true;
+          if (!mbar_wait(bar.tail(), 0, ab, p.status)) break;
+          zero_rows<D>(q_tile(i), (sp.nq - pos) * p.group);
+          zero_rows<D>(o_tile(i), (sp.nq - pos) * p.group);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar.full(i));
+        }
+      }
+      if (*ab) {  // leave no copy in flight
+        mbar_wait_settle(bar.kept(), 0);
+        if (tail_used) mbar_wait_settle(bar.tail(), 0);
+      }
+    } else if (warp == 2 && n > 0) {
+      // ---------------------------------- the rows' log-sum-exp and delta
+      for (int i = 0; i < n; ++i) {
+        if (i >= C::STAGES && !mbar_wait(bar.empty(i), ((i / C::STAGES) - 1) & 1, ab, p.status)) break;
+        const int pos = tile_pos(i);
+        float* lse = lse_of(i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = lane + 32 * e, at = r / p.group;
+          float2 t = make_float2(INFINITY, 0.f);  // a row that is not there: weights 0
+          if (at < P && pos + at < sp.nq)
+            t = p.terms[((long long)sp.q0 + pos + at) * p.hq + kh * p.group + (r - at * p.group)];
+          lse[r] = t.x;
+          lse[kTile + r] = t.y;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar.full(i));
+      }
+    } else if (warp == 1 && n > 0) {
+      // -------------------------------------------------------------- MMAs
+      if (lane == 0) {
+        bool ok = mbar_wait(bar.kept(), 0, ab, p.status) && mbar_wait(bar.full(0), 0, ab, p.status);
+        if (ok) {
+          tc_fence_after();
+          mma_rows_by_rows<D, BF16>(s_at, k_tile, q_tile(0));
+          mma_commit(bar.s());
+          mma_rows_by_rows<D, BF16>(dp_at, v_tile, o_tile(0));
+          mma_commit(bar.dp());
+          for (int i = 0; i < n; ++i) {
+            if (i + 1 < n && !mbar_wait(bar.full(i + 1), ((i + 1) / C::STAGES) & 1, ab, p.status)) break;
+            if (!mbar_wait(bar.p_ready(), i & 1, ab, p.status)) break;
+            tc_fence_after();
+            // the halves of P^T lie 64 columns apart
+            mma_halves_by_tile<D, BF16>(dv_at, s_at, o_tile(i), i > 0);
+            if (i + 1 < n) {
+              mma_rows_by_rows<D, BF16>(s_at, k_tile, q_tile(i + 1));
+              mma_commit(bar.s());
+            }
+            if (!mbar_wait(bar.ds_ready(), i & 1, ab, p.status)) break;
+            tc_fence_after();
+            mma_halves_by_tile<D, BF16>(dk_at, dp_at, q_tile(i), i > 0);
+            mma_commit(bar.empty(i));
+            if (i + 1 < n) {
+              mma_rows_by_rows<D, BF16>(dp_at, v_tile, o_tile(i + 1));
+              mma_commit(bar.dp());
+            }
+          }
+        }
+        mma_commit(bar.done());
+        mbar_wait_settle(bar.done(), 0);
+      }
+      __syncwarp();
+    }
+  } else {
+    regs_inc<C::REGS_WORK>();
+    // ------------------------------------------------- P^T, dS^T, epilogue
+    const int half = (warp >> 2) - 1, key = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t my_s = s_at + lanes + half * 64, my_dp = dp_at + lanes + half * 64;
+    const bool live = key < nk;
+    int lo, hi;  // positions that see this key
+    seen_by(p, sp, j0 + min(key, nk - 1), &lo, &hi);
+    // positions that see all keys of the warp, and those of any
+    const int all_lo = __reduce_max_sync(0xffffffffu, lo), all_hi = __reduce_min_sync(0xffffffffu, hi);
+    const float sl2 = p.scale * kLog2e;
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      // the terms were written before the copies' barrier completed, which the
+      // arrival of S^T follows; waiting for it makes them visible here
+      if (!(ok = mbar_wait(bar.full(i), (i / C::STAGES) & 1, ab, p.status))) break;
+      if (!(ok = mbar_wait(bar.s(), i & 1, ab, p.status))) break;
+      tc_fence_after();
+      const int pos = tile_pos(i);
+      const bool masked = pos < all_lo || pos + P > all_hi;
+      const int a = (lo - pos) * p.group - half * 64, b = (min(hi, pos + P) - pos) * p.group - half * 64;
+      const float4* lse = reinterpret_cast<const float4*>(lse_of(i) + half * 64);
+      const float4* delta = lse + kTile / 4;
+      uint32_t x[2][32];
+      tmem_ld32(my_s, x[0]);
+      tmem_ld32(my_s + 32, x[1]);
+      tmem_wait_ld_regs(x[0]);
+      tmem_wait_ld_regs(x[1]);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+          const float4 l = lse[8 * c + e / 4];
+          float f[4] = {__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]), __uint_as_float(x[c][e + 2]),
+                        __uint_as_float(x[c][e + 3])};
+          fma2(f[0], f[1], f[0], f[1], sl2, sl2, -l.x, -l.y);
+          fma2(f[2], f[3], f[2], f[3], sl2, sl2, -l.z, -l.w);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            f[u] = ex2(f[u]);
+            if (masked && !(32 * c + e + u >= a && 32 * c + e + u < b)) f[u] = 0.f;
+            x[c][e + u] = __float_as_uint(f[u]);
+          }
+          w[e / 2] = pack2<T>(f[0], f[1]);
+          w[e / 2 + 1] = pack2<T>(f[2], f[3]);
+        }
+        tmem_st16(my_s + 16 * c, w);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar.p_ready());
+      if (!(ok = mbar_wait(bar.dp(), i & 1, ab, p.status))) break;
+      tc_fence_after();
+      uint32_t y[2][32];
+      tmem_ld32(my_dp, y[0]);
+      tmem_ld32(my_dp + 32, y[1]);
+      tmem_wait_ld_regs(y[0]);
+      tmem_wait_ld_regs(y[1]);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+          const float4 l = delta[8 * c + e / 4];
+          float f[4] = {__uint_as_float(y[c][e]), __uint_as_float(y[c][e + 1]), __uint_as_float(y[c][e + 2]),
+                        __uint_as_float(y[c][e + 3])};
+          add2(f[0], f[1], f[0], f[1], -l.x, -l.y);
+          add2(f[2], f[3], f[2], f[3], -l.z, -l.w);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            f[u] *= __uint_as_float(x[c][e + u]);
+            if (masked && !(32 * c + e + u >= a && 32 * c + e + u < b)) f[u] = 0.f;
+          }
+          w[e / 2] = pack2<T>(f[0], f[1]);
+          w[e / 2 + 1] = pack2<T>(f[2], f[3]);
+        }
+        tmem_st16(my_dp + 16 * c, w);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar.ds_ready());
+    }
+    if (ok && n > 0) ok = mbar_wait(bar.done(), 0, ab, p.status);
+    if (ok) {
+      tc_fence_after();
+      // the first warpgroup writes dv, the second dk
+      const float f0 = half ? p.scale : 1.f;
+      const uint32_t from = (half ? dk_at : dv_at) + lanes;
+      const long long at = ((long long)(sp.k0 + j0 + key) * p.hk + kh) * D;
+      T* to = (T*)(half ? p.dk : p.dv) + at;
+      float* part = p.part_o + ((long long)z * 2 + half) * p.total_k * p.hk * D + at;
+      bool finite = true;
+      constexpr int W = D < 32 ? D : 32;
+#pragma unroll
+      for (int c = 0; c < D / W; ++c) {
+        uint32_t o[W] = {};
+        if (n > 0) tmem_ld_n<W>(from + W * c, o);
+        float f[W];
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          f[e] = __uint_as_float(o[e]) * f0;
+          finite = finite && fabsf(f[e]) < INFINITY;
+        }
+        if (live) {
+          if (Z > 1)
+            store_run<W>(part + W * c, f);
+          else
+            store_run<T, W>(to + W * c, f);
+        }
+      }
+      // keys with a result that is not finite are taken again, row by row
+      unsigned again = __ballot_sync(0xffffffffu, live && !finite);
+      while (again) {
+        const int src = __ffs(again) - 1;
+        again &= again - 1;
+        const int l0 = __shfl_sync(0xffffffffu, lo, src), h0 = __shfl_sync(0xffffffffu, hi, src);
+        const long long kat = __shfl_sync(0xffffffffu, at, src);
+        float acc[(D + 31) / 32] = {};
+        for (int i = 0; i < n; ++i) {
+          const long long r0 = (long long)max(tile_pos(i), l0) * p.group,
+                          r1 = (long long)min(tile_pos(i) + P, h0) * p.group;
+          for (long long r = r0; r < r1; r += 32) {
+            float wgt = 0.f, ds = 0.f;
+            const long long mine = min(r + lane, r1 - 1);
+            const long long row = ((long long)sp.q0 + mine / p.group) * p.hq + kh * p.group + mine % p.group;
+            if (r + lane < r1) exact_pair<T, D>(p, row, kat / D, &wgt, &ds);
+            for (int t = 0; t < (int)min(32ll, r1 - r); ++t) {
+              const float u = __shfl_sync(0xffffffffu, half ? ds : wgt, t);
+              const long long rt = __shfl_sync(0xffffffffu, row, t);
+              const T* src_row = (const T*)(half ? p.q : p.dout) + rt * D;
+#pragma unroll
+              for (int e = 0; e < (D + 31) / 32; ++e)
+                if (lane + 32 * e < D) acc[e] = fmaf(u, to_f<T>(src_row[lane + 32 * e]), acc[e]);
+            }
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < (D + 31) / 32; ++e) {
+          if (lane + 32 * e >= D) continue;
+          if (Z > 1)
+            p.part_o[((long long)z * 2 + half) * p.total_k * p.hk * D + kat + lane + 32 * e] = acc[e] * f0;
+          else
+            ((T*)(half ? p.dk : p.dv))[kat + lane + 32 * e] = from_f<T>(acc[e] * f0);
+        }
+      }
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Adds the pieces' dk and dv in order; slots of no sequence are left alone.
+template <typename T> __global__ void __launch_bounds__(256) packed_dkdv_join_kernel(PackedArgs p) {
+  const int vecs = p.d / 8;
+  const long long e = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long per = (long long)p.total_k * p.hk * vecs;
+  if (e >= per) return;
+  const int key = (int)(e / ((long long)p.hk * vecs));
+  int a = 0, b = p.nseq - 1;  // the last sequence that starts at or before the key
+  while (a < b) {
+    const int m = (a + b + 1) >> 1;
+    if (clamped(p.cu_k, m, p.total_k) <= key)
+      a = m;
+    else
+      b = m - 1;
+  }
+  const Span sp = span_of(p, a);
+  if (key < sp.k0 || key >= sp.k0 + sp.nk) return;
+  const int which = blockIdx.y;
+  const float* from = p.part_o + which * per * 8 + e * 8;
+  float f[8] = {};
+  for (int z = 0; z < p.max_pieces; ++z) {
+    const float4 u = *reinterpret_cast<const float4*>(from + (long long)z * 2 * per * 8);
+    const float4 v = *reinterpret_cast<const float4*>(from + (long long)z * 2 * per * 8 + 4);
+    f[0] += u.x, f[1] += u.y, f[2] += u.z, f[3] += u.w, f[4] += v.x, f[5] += v.y, f[6] += v.z, f[7] += v.w;
+  }
+  store_run<T, 8>((T*)(which ? p.dk : p.dv) + e * 8, f);
+}
+
+// ---------------------------------------------------------------------- dq
+template <typename T, int D>
+__global__ void __launch_bounds__(Bwd<D>::THREADS, 1)
+packed_dq_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mo,
+                    const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                    const PackedArgs p) {
+  using C = Bwd<D>;
+  using G = Geo<D>;
+  constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value;
+  extern __shared__ uint8_t raw[];
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  const int P = kTile / p.group, kh = blockIdx.y;
+  int s;
+  long long idx;
+  find_part_warp(p.cu_q, p.nseq, p.total_q, 1, P, blockIdx.x, &s, &idx);
+  const Span sp = span_of(p, s);
+  const long long part = (sp.nq + P - 1) / P - 1 - idx;  // the rows that see most keys first
+  if (idx < 0 || part < 0) return;
+  const int pos0 = (int)part * P;
+  int kb, ke, unused;
+  visible(p, sp, pos0, &kb, &unused);
+  visible(p, sp, min(pos0 + P, sp.nq) - 1, &unused, &ke);
+  const int n = ke > kb ? (ke - kb + kTile - 1) / kTile : 0;
+
+  const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
+  const uint32_t q_tile = base, o_tile = base + G::TILE_BYTES;
+  auto k_tile = [&](int i) { return base + C::RING_OFF + (i % C::STAGES) * 2 * G::TILE_BYTES; };
+  auto v_tile = [&](int i) { return k_tile(i) + G::TILE_BYTES; };
+  const Bars bar{base + C::BAR_OFF, C::STAGES};
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    bar.init(1);
+  }
+  if (warp == 1) tmem_alloc(smem_addr(&tmem_slot), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const uint32_t dp_at = tmem + 256, dq_at = tmem + 384;  // S in two slots of 128 columns
+  volatile int* ab = &abort_flag;
+
+  if (warp < 4) {
+    regs_dec<C::REGS_CTRL>();
+    if (warp == 0 && n > 0) {
+      // ------------------------------------------------------------- loads
+      if (lane == 0) {
+        mbar_expect_tx(bar.kept(), (uint32_t)(2 * P * p.group * D * 2));
+        load_row_tile<D>(q_tile, &mq, bar.kept(), kh, sp.q0 + pos0);
+        load_row_tile<D>(o_tile, &mo, bar.kept(), kh, sp.q0 + pos0);
+      }
+      bool tail_used = false;
+      int i = 0;
+      for (; i < n; ++i) {
+        if (i >= C::STAGES && !mbar_wait(bar.empty(i), ((i / C::STAGES) - 1) & 1, ab, p.status)) break;
+        const int k0 = kb + i * kTile;
+        const bool tail = k0 + kTile > sp.nk;  // keys past the sequence are zeroed
+        const uint32_t b = tail ? bar.tail() : bar.full(i);
+        if (lane == 0) {
+          mbar_expect_tx(b, 2 * G::TILE_BYTES);
+          load_key_tile<D>(k_tile(i), &mk, b, kh, sp.k0 + k0);
+          load_key_tile<D>(v_tile(i), &mv, b, kh, sp.k0 + k0);
+        }
+        __syncwarp();
+        if (tail) {
+          tail_used = true;
+          if (!mbar_wait(bar.tail(), 0, ab, p.status)) break;
+          zero_rows<D>(k_tile(i), sp.nk - k0);
+          zero_rows<D>(v_tile(i), sp.nk - k0);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar.full(i));
+        }
+      }
+      if (*ab) {  // leave no copy in flight
+        mbar_wait_settle(bar.kept(), 0);
+        if (tail_used) mbar_wait_settle(bar.tail(), 0);
+        for (int u = max(0, i - C::STAGES); u < i; ++u) mbar_wait_settle(bar.full(u), (u / C::STAGES) & 1);
+      }
+    } else if (warp == 1 && n > 0) {
+      // -------------------------------------------------------------- MMAs
+      if (lane == 0) {
+        bool ok = mbar_wait(bar.kept(), 0, ab, p.status) && mbar_wait(bar.full(0), 0, ab, p.status);
+        if (ok) {
+          tc_fence_after();
+          mma_rows_by_rows<D, BF16>(tmem, q_tile, k_tile(0));
+          mma_commit(bar.s());
+          mma_rows_by_rows<D, BF16>(dp_at, o_tile, v_tile(0));
+          mma_commit(bar.dp());
+          for (int i = 0; i < n; ++i) {
+            if (i + 1 < n) {
+              if (!mbar_wait(bar.full(i + 1), ((i + 1) / C::STAGES) & 1, ab, p.status)) break;
+              tc_fence_after();
+              mma_rows_by_rows<D, BF16>(tmem + ((i + 1) & 1) * kTile, q_tile, k_tile(i + 1));
+              mma_commit(bar.s());
+            }
+            if (!mbar_wait(bar.ds_ready(), i & 1, ab, p.status)) break;
+            tc_fence_after();
+            if (i + 1 < n) {
+              mma_rows_by_rows<D, BF16>(dp_at, o_tile, v_tile(i + 1));
+              mma_commit(bar.dp());
+            }
+            mma_halves_by_tile<D, BF16>(dq_at, tmem + (i & 1) * kTile, k_tile(i), i > 0);
+            mma_commit(bar.empty(i));
+          }
+        }
+        mma_commit(bar.done());
+        mbar_wait_settle(bar.done(), 0);
+      }
+      __syncwarp();
+    }
+  } else {
+    regs_inc<C::REGS_WORK>();
+    // ------------------------------------------------------- dS, epilogue
+    const int half = (warp >> 2) - 1, row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const int at = row / p.group, pos = pos0 + at;
+    const bool live = at < P && pos < sp.nq;
+    const long long out_row = ((long long)sp.q0 + (live ? pos : pos0)) * p.hq + kh * p.group + (live ? row - at * p.group : 0);
+    int lo, hi;
+    visible(p, sp, live ? pos : pos0, &lo, &hi);
+    const int all_lo = __reduce_max_sync(0xffffffffu, lo), all_hi = __reduce_min_sync(0xffffffffu, hi);
+    const float2 term = p.terms[out_row];
+    const float sl2 = p.scale * kLog2e;
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      const uint32_t my_s = tmem + lanes + (i & 1) * kTile + half * 64, my_dp = dp_at + lanes + half * 64;
+      if (!(ok = mbar_wait(bar.s(), i & 1, ab, p.status))) break;
+      tc_fence_after();
+      const int k0 = kb + i * kTile;
+      const bool masked = k0 < all_lo || k0 + kTile > all_hi;
+      const int a = lo - k0 - half * 64, b = hi - k0 - half * 64;
+      uint32_t x[2][32];
+      tmem_ld32(my_s, x[0]);
+      tmem_ld32(my_s + 32, x[1]);
+      tmem_wait_ld_regs(x[0]);
+      tmem_wait_ld_regs(x[1]);
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          float f0 = __uint_as_float(x[c][e]), f1 = __uint_as_float(x[c][e + 1]);
+          fma2(f0, f1, f0, f1, sl2, sl2, -term.x, -term.x);
+          x[c][e] = __float_as_uint(ex2(f0));
+          x[c][e + 1] = __float_as_uint(ex2(f1));
+        }
+      if (!(ok = mbar_wait(bar.dp(), i & 1, ab, p.status))) break;
+      tc_fence_after();
+      uint32_t y[2][32];
+      tmem_ld32(my_dp, y[0]);
+      tmem_ld32(my_dp + 32, y[1]);
+      tmem_wait_ld_regs(y[0]);
+      tmem_wait_ld_regs(y[1]);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          float f0 = __uint_as_float(y[c][e]), f1 = __uint_as_float(y[c][e + 1]);
+          add2(f0, f1, f0, f1, -term.y, -term.y);
+          f0 *= __uint_as_float(x[c][e]);
+          f1 *= __uint_as_float(x[c][e + 1]);
+          if (masked) {
+            if (!(32 * c + e >= a && 32 * c + e < b)) f0 = 0.f;
+            if (!(32 * c + e + 1 >= a && 32 * c + e + 1 < b)) f1 = 0.f;
+          }
+          w[e / 2] = pack2<T>(f0, f1);
+        }
+        tmem_st16(my_s + 16 * c, w);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar.ds_ready());
+    }
+    if (ok && n > 0) ok = mbar_wait(bar.done(), 0, ab, p.status);
+    if (ok) {
+      tc_fence_after();
+      // each warpgroup writes half of the columns
+      constexpr int H = D / 2, W = H < 32 ? H : 32;
+      T* to = (T*)p.dq + out_row * D + half * H;
+      bool finite = true;
+#pragma unroll
+      for (int c = 0; c < H / W; ++c) {
+        uint32_t o[W] = {};
+        if (n > 0) tmem_ld_n<W>(dq_at + lanes + half * H + W * c, o);
+        float f[W];
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          f[e] = __uint_as_float(o[e]) * p.scale;
+          finite = finite && fabsf(f[e]) < INFINITY;
+        }
+        if (live) store_run<T, W>(to + W * c, f);
+      }
+      // rows with a result that is not finite are taken again, key by key
+      unsigned again = __ballot_sync(0xffffffffu, live && !finite);
+      while (again) {
+        const int src = __ffs(again) - 1;
+        again &= again - 1;
+        const int l0 = __shfl_sync(0xffffffffu, lo, src), h0 = __shfl_sync(0xffffffffu, hi, src);
+        const long long r = __shfl_sync(0xffffffffu, out_row, src);
+        float acc[(D + 31) / 32] = {};
+        for (int j = l0; j < h0; j += 32) {
+          float wgt, ds = 0.f;
+          if (j + lane < h0) exact_pair<T, D>(p, r, (long long)(sp.k0 + j + lane) * p.hk + kh, &wgt, &ds);
+          for (int t = 0; t < min(32, h0 - j); ++t) {
+            const float u = __shfl_sync(0xffffffffu, ds, t);
+            const T* key = (const T*)p.k + ((long long)(sp.k0 + j + t) * p.hk + kh) * D;
+#pragma unroll
+            for (int e = 0; e < (D + 31) / 32; ++e)
+              if (lane + 32 * e < D) acc[e] = fmaf(u, to_f<T>(key[lane + 32 * e]), acc[e]);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < (D + 31) / 32; ++e) {
+          const int c = lane + 32 * e;
+          if (c >= half * H && c < half * H + H) ((T*)p.dq)[r * D + c] = from_f<T>(acc[e] * p.scale);
+        }
+      }
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <typename T, int D> cudaError_t launch(const PackedArgs& p, cudaStream_t st) {
+  using C = Bwd<D>;
+  constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
+  constexpr int kRegs = 128 * C::REGS_CTRL + 256 * C::REGS_WORK;
+  const long long kb = part_numbers(p.nseq, p.total_k, 1, kTile);
+  const long long qb = part_numbers(p.nseq, p.total_q, 1, kTile / p.group);
+  if (kb > 0x7fffffffLL || qb > 0x7fffffffLL) return cudaErrorInvalidValue;
+  cudaError_t e = prepare_kernel<packed_dkdv_tc_kernel<T, D>>(C::SMEM_ASKED, C::THREADS, kRegs);
+  if (e == cudaSuccess) e = prepare_kernel<packed_dq_tc_kernel<T, D>>(C::SMEM_ASKED, C::THREADS, kRegs);
+  if (e != cudaSuccess) return e;
+  CUtensorMap mq, mo, mk, mv;
+  if (!row_map(&mq, p.q, p, bf16) || !row_map(&mo, p.dout, p, bf16) || !key_map(&mk, p.k, p, bf16) ||
+      !key_map(&mv, p.v, p, bf16))
+    return cudaErrorInvalidValue;
+  packed_dkdv_tc_kernel<T, D><<<dim3((unsigned)kb, (unsigned)p.hk, (unsigned)p.max_pieces), C::THREADS,
+                                C::SMEM_ASKED, st>>>(mq, mo, mk, mv, p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (p.max_pieces > 1) {
+    const long long blocks = ((long long)p.total_k * p.hk * (D / 8) + 255) / 256;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    packed_dkdv_join_kernel<T><<<dim3((unsigned)blocks, 2), 256, 0, st>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  packed_dq_tc_kernel<T, D><<<dim3((unsigned)qb, (unsigned)p.hk), C::THREADS, C::SMEM_ASKED, st>>>(mq, mo, mk, mv, p);
+  return cudaGetLastError();
+}
+template <typename T> cudaError_t launch_d(const PackedArgs& p, cudaStream_t st) {
+  switch (p.d) {
+    case 16: return launch<T, 16>(p, st);
+    case 32: return launch<T, 32>(p, st);
+    case 64: return launch<T, 64>(p, st);
+    case 128: return launch<T, 128>(p, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_packed_backward_tc(const PackedArgs& p, na_dtype dt, cudaStream_t st) {
+  return dt == NA_F16 ? launch_d<__half>(p, st) : launch_d<__nv_bfloat16>(p, st);
+}
+
+}  // namespace na2d
