@@ -326,8 +326,11 @@ template <typename T, int D> __global__ void __launch_bounds__(256) packed_terms
   }
 #pragma unroll
   for (int o = 1; o < LPR; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (live && v == 0)
-    p.terms[row] = make_float2(p.lse_in[row % p.hq * p.total_q + row / p.hq] * kLog2e, s);
+  if (live && v == 0) {
+    const float lse = p.lse_in[row % p.hq * p.total_q + row / p.hq];
+    // a row that sees no key has no weights, whatever its gradient holds
+    p.terms[row] = lse == -INFINITY ? make_float2(INFINITY, 0.f) : make_float2(lse * kLog2e, s);
+  }
 }
 
 template <int D> constexpr int bwd_smem() {

@@ -35,37 +35,55 @@ template <int D> struct Geo {
   static constexpr uint32_t LAYOUT = ROWB == 128 ? kLayoutSW128 : ROWB == 64 ? kLayoutSW64 : kLayoutSW32;
 };
 
-// Step kk of 16 columns of a tile read as a K-major operand (rows x D).
-template <int D> NA_DEVICE uint64_t k_major(uint32_t tile, int kk) {
+// Operand descriptors, split in halves: the low word holds the address and the
+// leading offset, so that a step inside a tile is one 32-bit addition; the
+// high word is a constant.  One thread issues all MMAs of a block, and what it
+// computes between two of them is time that the tensor pipe may wait.
+template <int D> struct KMajor {  // rows x D, 16 columns a step
   using G = Geo<D>;
-  constexpr int PER = G::COLS / 16;
-  return smem_desc(tile + (kk / PER) * G::BLOCK_BYTES + (kk % PER) * 32, 16, 8 * G::ROWB, G::LAYOUT);
+  static constexpr uint32_t HI = (8 * G::ROWB >> 4) | 1u << 14 | G::LAYOUT << 29;
+  static constexpr int PER = G::COLS / 16;
+  NA_DEVICE static uint32_t lo(uint32_t tile) { return (tile >> 4) | 1u << 16; }
+  static constexpr uint32_t step(int kk) { return ((kk / PER) * G::BLOCK_BYTES + (kk % PER) * 32) >> 4; }
+};
+template <int D> struct MnMajor {  // D x rows, 16 rows a step
+  using G = Geo<D>;
+  static constexpr uint32_t HI = KMajor<D>::HI;
+  NA_DEVICE static uint32_t lo(uint32_t tile) { return (tile >> 4) | (uint32_t)(G::BLOCK_BYTES >> 4) << 16; }
+  static constexpr uint32_t step(int kk) { return (kk * 16 * G::ROWB) >> 4; }
+};
+NA_DEVICE void mma_ss_lo(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.b32 p, %5, 0;\n mov.b64 x, {%1, %3};\n mov.b64 y, {%2, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
 }
-// Step kk of 16 rows of a tile read as an MN-major operand (D x rows).
-template <int D> NA_DEVICE uint64_t mn_major(uint32_t tile, int kk) {
-  using G = Geo<D>;
-  return smem_desc(tile + kk * 16 * G::ROWB, G::BLOCK_BYTES, 8 * G::ROWB, G::LAYOUT);
+NA_DEVICE void mma_ts_lo(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.b32 p, %5, 0;\n mov.b64 y, {%2, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
 }
 
 // D[128 x 128] = A B^T over D columns, both tiles K-major.
 template <int D, bool BF16> NA_DEVICE void mma_rows_by_rows(uint32_t d, uint32_t a, uint32_t b) {
   constexpr uint32_t idesc = idesc_f16(BF16, kTile, kTile, false);
+  const uint32_t x = KMajor<D>::lo(a), y = KMajor<D>::lo(b);
 #pragma unroll
-  for (int kk = 0; kk < D / 16; ++kk) mma_ss(d, k_major<D>(a, kk), k_major<D>(b, kk), idesc, kk > 0);
+  for (int kk = 0; kk < D / 16; ++kk)
+    mma_ss_lo(d, x + KMajor<D>::step(kk), y + KMajor<D>::step(kk), KMajor<D>::HI, idesc, kk > 0);
 }
-// D[128 x D] (+)= A B, A 128 x 128 of 16 bits in tensor memory, B a tile.
-template <int D, bool BF16> NA_DEVICE void mma_weights_by_tile(uint32_t d, uint32_t a, uint32_t b, bool add) {
+// D[128 x D] (+)= A B, A 128 x 128 of 16 bits in tensor memory, B a tile; the
+// second half of A's columns begins `gap` columns after the first.
+template <int D, bool BF16, int GAP = 32>
+NA_DEVICE void mma_weights_by_tile(uint32_t d, uint32_t a, uint32_t b, bool add) {
   constexpr uint32_t idesc = idesc_f16(BF16, kTile, D, true);
-#pragma unroll
-  for (int kk = 0; kk < kTile / 16; ++kk) mma_ts(d, a + kk * 8, mn_major<D>(b, kk), idesc, (add || kk > 0) ? 1u : 0u);
-}
-
-// The same with the operand's two halves of 64 in tensor memory 64 columns apart.
-template <int D, bool BF16> NA_DEVICE void mma_halves_by_tile(uint32_t d, uint32_t a, uint32_t b, bool add) {
-  constexpr uint32_t idesc = idesc_f16(BF16, kTile, D, true);
+  const uint32_t y = MnMajor<D>::lo(b);
 #pragma unroll
   for (int kk = 0; kk < kTile / 16; ++kk)
-    mma_ts(d, a + (kk / 4) * 64 + (kk % 4) * 8, mn_major<D>(b, kk), idesc, (add || kk > 0) ? 1u : 0u);
+    mma_ts_lo(d, a + (kk / 4) * GAP + (kk % 4) * 8, y + MnMajor<D>::step(kk), MnMajor<D>::HI, idesc, add || kk > 0);
 }
 
 // All column blocks of 128 keys from key `row` on of head kh.

@@ -83,6 +83,15 @@ template <int W> NA_DEVICE void tmem_ld_n(uint32_t at, uint32_t (&r)[W]) {
   tmem_wait_ld_regs(r);
 }
 
+// Columns outside [a, b) become `to`.
+NA_DEVICE void mask_outside(uint32_t (&x)[2][32], int a, int b, uint32_t to) {
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (32 * c + e < a || 32 * c + e >= b) x[c][e] = to;
+}
+
 // A store of W consecutive results, in dt or in float32.
 template <typename T, int W> NA_DEVICE void store_run(T* to, const float (&f)[W]) {
 #pragma unroll
@@ -226,14 +235,14 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
             if (!mbar_wait(bar.p_ready(), i & 1, ab, p.status)) break;
             tc_fence_after();
             // the halves of P^T lie 64 columns apart
-            mma_halves_by_tile<D, BF16>(dv_at, s_at, o_tile(i), i > 0);
+            mma_weights_by_tile<D, BF16, 64>(dv_at, s_at, o_tile(i), i > 0);
             if (i + 1 < n) {
               mma_rows_by_rows<D, BF16>(s_at, k_tile, q_tile(i + 1));
               mma_commit(bar.s());
             }
             if (!mbar_wait(bar.ds_ready(), i & 1, ab, p.status)) break;
             tc_fence_after();
-            mma_halves_by_tile<D, BF16>(dk_at, dp_at, q_tile(i), i > 0);
+            mma_weights_by_tile<D, BF16, 64>(dk_at, dp_at, q_tile(i), i > 0);
             mma_commit(bar.empty(i));
             if (i + 1 < n) {
               mma_rows_by_rows<D, BF16>(dp_at, v_tile, o_tile(i + 1));
@@ -275,6 +284,7 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       tmem_ld32(my_s + 32, x[1]);
       tmem_wait_ld_regs(x[0]);
       tmem_wait_ld_regs(x[1]);
+      if (masked) mask_outside(x, a, b, 0xff800000u);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         uint32_t w[16];
@@ -288,7 +298,6 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             f[u] = ex2(f[u]);
-            if (masked && !(32 * c + e + u >= a && 32 * c + e + u < b)) f[u] = 0.f;
             x[c][e + u] = __float_as_uint(f[u]);
           }
           w[e / 2] = pack2<T>(f[0], f[1]);
@@ -307,6 +316,8 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       tmem_ld32(my_dp + 32, y[1]);
       tmem_wait_ld_regs(y[0]);
       tmem_wait_ld_regs(y[1]);
+      // a zero weight does not stop a NaN
+      if (masked) mask_outside(y, a, b, 0u);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         uint32_t w[16];
@@ -318,10 +329,7 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
           add2(f[0], f[1], f[0], f[1], -l.x, -l.y);
           add2(f[2], f[3], f[2], f[3], -l.z, -l.w);
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            f[u] *= __uint_as_float(x[c][e + u]);
-            if (masked && !(32 * c + e + u >= a && 32 * c + e + u < b)) f[u] = 0.f;
-          }
+          for (int u = 0; u < 4; ++u) f[u] *= __uint_as_float(x[c][e + u]);
           w[e / 2] = pack2<T>(f[0], f[1]);
           w[e / 2 + 1] = pack2<T>(f[2], f[3]);
         }
@@ -536,7 +544,7 @@ packed_dq_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
               mma_rows_by_rows<D, BF16>(dp_at, o_tile, v_tile(i + 1));
               mma_commit(bar.dp());
             }
-            mma_halves_by_tile<D, BF16>(dq_at, tmem + (i & 1) * kTile, k_tile(i), i > 0);
+            mma_weights_by_tile<D, BF16, 64>(dq_at, tmem + (i & 1) * kTile, k_tile(i), i > 0);
             mma_commit(bar.empty(i));
           }
         }
@@ -571,6 +579,7 @@ packed_dq_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
       tmem_ld32(my_s + 32, x[1]);
       tmem_wait_ld_regs(x[0]);
       tmem_wait_ld_regs(x[1]);
+      if (masked) mask_outside(x, a, b, 0xff800000u);
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -587,6 +596,7 @@ packed_dq_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
       tmem_ld32(my_dp + 32, y[1]);
       tmem_wait_ld_regs(y[0]);
       tmem_wait_ld_regs(y[1]);
+      if (masked) mask_outside(y, a, b, 0u);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         uint32_t w[16];
@@ -596,10 +606,6 @@ packed_dq_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
           add2(f0, f1, f0, f1, -term.y, -term.y);
           f0 *= __uint_as_float(x[c][e]);
           f1 *= __uint_as_float(x[c][e + 1]);
-          if (masked) {
-            if (!(32 * c + e >= a && 32 * c + e < b)) f0 = 0.f;
-            if (!(32 * c + e + 1 >= a && 32 * c + e + 1 < b)) f1 = 0.f;
-          }
           w[e / 2] = pack2<T>(f0, f1);
         }
         tmem_st16(my_s + 16 * c, w);
