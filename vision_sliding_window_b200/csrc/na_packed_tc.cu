@@ -4,22 +4,26 @@
 // A block owns two row tiles (A and B) of one key head and walks the keys they
 // see in tiles of 128:
 //
-//   S_t = Q_t K_j^T  ->  P_t = 2^(S_t scale log2e - ref), 16 bits over S_t's
-//   columns  ->  O_t += P_t V_j        (S, P and O in tensor memory)
+//   S_t = Q_t K_j^T  ->  P_t = 2^(S_t scale log2e - ref) in 16 bits
+//   ->  O_t += P_t V_j                        (S, P and O in tensor memory)
 //
-// with one softmax warpgroup a tile, a thread a row.  While one tile's
-// softmax runs, the tensor pipe works for the other, so both the special
-// functions and the tensor cores stay busy; with one row tile a block they
-// would wait for each other.  O is rescaled only when a row's maximum has
-// grown by 2^8 over its reference: P then stays below 2^8, far inside the
-// 16-bit types, and most tiles rescale nothing; the softmax warps do it
-// themselves, as S_t's arrival implies that the last P V of t is done.
+// with one softmax warpgroup a tile, a thread a row.  A softmax takes S into
+// registers at once, and the next S is made while it works, so that a tile's
+// chain is its softmax alone and the products hide behind it.  That needs P in
+// columns of its own; at d = 128 tensor memory then has room for one S, which
+// the tiles use in turn (each holds it for its product and the load, about 0.8
+// of 2 thousand cycles).  With P over S, softmax and products of a tile took
+// turns: 3.3 thousand cycles a step where the tensor pipe needs 2.0.
+//
+// O is rescaled only when a row's maximum has grown by 2^8 over its reference:
+// P then stays below 2^8, far inside the 16-bit types, and most tiles rescale
+// nothing; the softmax warps do it themselves.
 //
 // P is rounded to the input type for its product with V; its sum is taken
 // before that, in float32.
 //
-// Roles: warp 0 loads (TMA), warp 1 issues the MMAs, warpgroups 1 and 2 are
-// the softmax and the epilogue of tiles A and B.
+// Roles: warp 0 loads (TMA), warp 1 issues S, warp 2 issues P V, warpgroups 1
+// and 2 are the softmax and the epilogue of tiles A and B.
 #include "na_packed_tc.cuh"
 
 namespace na2d {
@@ -39,7 +43,10 @@ template <int D> struct Fwd {
   static_assert(SMEM <= kMaxSmem, "fits");
   static constexpr int THREADS = 384;
   static constexpr int REGS_CTRL = 72, REGS_SOFTMAX = 216;
-  static constexpr int O_COL = 256;  // S_A at 0, S_B at 128, O_t at 256 + t D
+  // tensor memory: one or two S of 128 columns, P_t of 64, O_t of d
+  static constexpr int S_BUFS = D == 128 ? 1 : 2;
+  static constexpr int P_COL = S_BUFS * kTile, O_COL = P_COL + 2 * 64;
+  static_assert(O_COL + 2 * D <= 512, "fits");
 };
 
 constexpr float kSlack = 8.f;  // log2 of how far a maximum may pass its reference
@@ -104,10 +111,12 @@ packed_forward_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_co
   auto bar_q = [&]() { return bars; };
   auto bar_full = [&](int i) { return bars + 8 + (i % SLOTS) * 8; };
   auto bar_empty = [&](int i) { return bars + 8 + (SLOTS + i % SLOTS) * 8; };
-  auto bar_s = [&](int t) { return bars + 8 + (2 * SLOTS + t) * 8; };
-  auto bar_p = [&](int t) { return bars + 8 + (2 * SLOTS + 2 + t) * 8; };
-  auto bar_o = [&](int t) { return bars + 8 + (2 * SLOTS + 4 + t) * 8; };
-  const uint32_t bar_tail = bars + 8 + (2 * SLOTS + 6) * 8, bar_done = bar_tail + 8;
+  auto bar_s = [&](int t) { return bars + 8 + (2 * SLOTS + t) * 8; };       // S_t is made
+  auto bar_pv = [&](int t) { return bars + 8 + (2 * SLOTS + 2 + t) * 8; };  // O_t has P_t V
+  auto bar_p = [&](int t, int half) { return bars + 8 + (2 * SLOTS + 4 + 2 * t + half) * 8; };
+  auto bar_free = [&](int b) { return bars + 8 + (2 * SLOTS + 8 + b) * 8; };  // an S is in registers
+  const uint32_t bar_tail = bars + 8 + (2 * SLOTS + 10) * 8, bar_done0 = bar_tail + 8;
+  auto bar_done = [&](int w) { return bar_done0 + w * 8; };
   if (threadIdx.x == 0) {
     abort_flag = 0;
     mbar_init(bar_q(), 1);
@@ -117,11 +126,14 @@ packed_forward_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_co
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar_s(t), 1);
-      mbar_init(bar_p(t), 4);
-      mbar_init(bar_o(t), 1);
+      mbar_init(bar_p(t, 0), 4);
+      mbar_init(bar_p(t, 1), 4);
+      mbar_init(bar_pv(t), 1);
+      mbar_init(bar_free(t), 4);
     }
     mbar_init(bar_tail, 1);
-    mbar_init(bar_done, 1);
+    mbar_init(bar_done(0), 1);
+    mbar_init(bar_done(1), 1);
     mbar_init_fence();
   }
   if (warp == 1) tmem_alloc(smem_addr(&tmem_slot), 512);
@@ -135,6 +147,9 @@ packed_forward_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_co
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   volatile int* ab = &abort_flag;
+  // fp16 weights are lifted by 2^7, which the sum takes out again: with the
+  // slack they stay below 2^15, and small ones keep their bits
+  constexpr float kLift = BF16 ? 0.f : 7.f;
 
   if (warp < 4) {
     regs_dec<C::REGS_CTRL>();
@@ -174,39 +189,56 @@ packed_forward_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_co
         for (int u = max(0, i - SLOTS); u < i; ++u) mbar_wait_settle(bar_full(u), (u / SLOTS) & 1);
       }
     } else if (warp == 1 && n > 0) {
-      // -------------------------------------------------------------- MMAs
-      if (lane == 0) {
-        auto s_mma = [&](int t, int j) {
-          mma_rows_by_rows<D, BF16>(tmem + t * kTile, q_tile(t), slot(2 * j));
-          mma_commit(bar_s(t));
-        };
-        bool ok = mbar_wait(bar_q(), 0, ab, p.status) && mbar_wait(bar_full(0), 0, ab, p.status);
-        if (ok) {
+      // ----------------------------------------------------------- S = Q K^T
+      // The whole warp walks the steps, which keeps what the operands are made
+      // of in uniform registers, and one lane issues.
+      bool ok = mbar_wait(bar_q(), 0, ab, p.status);
+      int used[2] = {0, 0};  // of each S
+      for (int j = 0; j < n; ++j) {
+        ok = ok && mbar_wait(bar_full(2 * j), (2 * j / SLOTS) & 1, ab, p.status);
+        for (int t = 0; t < 2; ++t) {
+          if (j >= steps[t]) continue;
+          const int b = C::S_BUFS == 1 ? 0 : t;
+          if (used[b] > 0) ok = ok && mbar_wait(bar_free(b), (used[b] - 1) & 1, ab, p.status);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          ++used[b];
           tc_fence_after();
-          for (int t = 0; t < 2; ++t)
-            if (steps[t] > 0) s_mma(t, 0);
-          mma_commit(bar_empty(0));
-          for (int j = 0; j < n && ok; ++j) {
-            if (!(ok = mbar_wait(bar_full(2 * j + 1), ((2 * j + 1) / SLOTS) & 1, ab, p.status))) break;
-            if (j + 1 < n && !(ok = mbar_wait(bar_full(2 * j + 2), ((2 * j + 2) / SLOTS) & 1, ab, p.status))) break;
-            for (int t = 0; t < 2; ++t) {
-              if (j >= steps[t]) continue;
-              if (!(ok = mbar_wait(bar_p(t), j & 1, ab, p.status))) break;
-              tc_fence_after();
-              mma_weights_by_tile<D, BF16>(tmem + C::O_COL + t * D, tmem + t * kTile, slot(2 * j + 1), j > 0);
-              if (j + 1 < steps[t])
-                s_mma(t, j + 1);
-              else
-                mma_commit(bar_o(t));
-            }
-            mma_commit(bar_empty(2 * j + 1));
-            if (j + 1 < n) mma_commit(bar_empty(2 * j + 2));
+          if (elect_one()) {
+            mma_rows_by_rows<D, BF16>(tmem + b * kTile, q_tile(t), slot(2 * j));
+            mma_commit(bar_s(t));
           }
         }
-        // every MMA has finished before tensor memory is freed
-        mma_commit(bar_done);
-        mbar_wait_settle(bar_done, 0);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        if (elect_one()) mma_commit(bar_empty(2 * j));
       }
+      // every MMA has finished before tensor memory is freed
+      if (elect_one()) mma_commit(bar_done(0));
+      mbar_wait_settle(bar_done(0), 0);
+      __syncwarp();
+    } else if (warp == 2 && n > 0) {
+      // ---------------------------------------------------------- O += P V
+      bool ok = true;
+      for (int j = 0; j < n && ok; ++j) {
+        ok = mbar_wait(bar_full(2 * j + 1), ((2 * j + 1) / SLOTS) & 1, ab, p.status);
+        for (int t = 0; t < 2; ++t) {
+          if (j >= steps[t]) continue;
+          const uint32_t o = tmem + C::O_COL + t * D, w = tmem + C::P_COL + t * 64;
+          ok = ok && mbar_wait(bar_p(t, 0), j & 1, ab, p.status);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          tc_fence_after();
+          if (elect_one()) mma_weights_by_tile<D, BF16, 32, 0, 4>(o, w, slot(2 * j + 1), j > 0);
+          ok = mbar_wait(bar_p(t, 1), j & 1, ab, p.status);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            mma_weights_by_tile<D, BF16, 32, 4, 8>(o, w, slot(2 * j + 1), true);
+            mma_commit(bar_pv(t));
+          }
+        }
+        if (ok && elect_one()) mma_commit(bar_empty(2 * j + 1));
+      }
+      if (elect_one()) mma_commit(bar_done(1));
+      mbar_wait_settle(bar_done(1), 0);
       __syncwarp();
     }
   } else {
@@ -214,7 +246,9 @@ packed_forward_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_co
     // ---------------------------------------------------- softmax, epilogue
     const int t = (warp >> 2) - 1, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_at = tmem + lanes + t * kTile, o_at = tmem + lanes + C::O_COL + t * D;
+    const int buf = C::S_BUFS == 1 ? 0 : t;
+    const uint32_t s_at = tmem + lanes + buf * kTile, w_at = tmem + lanes + C::P_COL + t * 64;
+    const uint32_t o_at = tmem + lanes + C::O_COL + t * D;
     const int at = row / p.group;  // position in the tile
     const int pos = pos0 + t * P + at;
     const bool live = at < P && pos < sp.nq;
@@ -236,8 +270,12 @@ packed_forward_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_co
       for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, x[c]);
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_wait_ld_regs(x[c]);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_free(buf));
       const int k0 = kb + j * kTile;
-      if (k0 < all_lo || k0 + kTile > all_hi) {
+      const bool masked = k0 < all_lo || k0 + kTile > all_hi;
+      if (masked) {
         const int a = lo - k0, b = hi - k0;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
@@ -250,15 +288,21 @@ packed_forward_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_co
       for (int c = 0; c < 4; ++c) {
         m4[c] = __uint_as_float(x[c][0]);
 #pragma unroll
-        for (int i = 1; i < 31; i += 2) m4[c] = max3(m4[c], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
-        m4[c] = fmaxf(m4[c], __uint_as_float(x[c][31]));
+        for (int i = 1; i < 31; i += 2)
+          m4[c] = max3_nan(m4[c], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
+        m4[c] = max_nan(m4[c], __uint_as_float(x[c][31]));
       }
-      const float top = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
+      const float top = max_nan(max3_nan(m4[0], m4[1], m4[2]), m4[3]);
+      // the last product has read P, and O can be changed
+      if (j > 0 && !(ok = mbar_wait(bar_pv(t), (j - 1) & 1, ab, p.status))) break;
+      tc_fence_after();
       if (j == 0) {
         ref = top;
-      } else if (__any_sync(0xffffffffu, (top - ref) * sl2 > kSlack)) {
-        // -inf - -inf is NaN and compares false: nothing seen yet stays so
-        const float next = fmaxf(ref, top);
+      } else if (__any_sync(0xffffffffu, live && !((top - ref) * sl2 <= kSlack))) {
+        // Rows that are not the sequence's have no say, or its bits would depend
+        // on them.  Also where nothing was seen yet (-inf - -inf) and for NaN, which
+        // makes the row's whole result NaN
+        const float next = max_nan(ref, top);
         const float f = ref == next ? 1.f : exp2f((ref - next) * sl2);
         ref = next;
         sum *= f;
@@ -273,35 +317,50 @@ packed_forward_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_co
           if constexpr (W == 32) tmem_st32(o_at + W * c, o); else tmem_st16(o_at, o);
         }
       }
-      const float shift = ref == -INFINITY ? 0.f : -ref * sl2;
+      // an infinite reference makes the whole row NaN, as inf - inf does
+      const float shift = ref == -INFINITY ? 0.f : fmaf(-ref, sl2, ref - ref) + kLift;
       float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+      auto weights = [&](auto poly) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t w[16];
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          float a0 = __uint_as_float(x[c][i]), a1 = __uint_as_float(x[c][i + 1]);
-          float b0 = __uint_as_float(x[c][i + 2]), b1 = __uint_as_float(x[c][i + 3]);
-          fma2(a0, a1, a0, a1, sl2, sl2, shift, shift);
-          fma2(b0, b1, b0, b1, sl2, sl2, shift, shift);
-          a0 = ex2(a0);
-          a1 = ex2(a1);
-          b0 = ex2(b0);
-          b1 = ex2(b1);
-          add2(s0, s1, s0, s1, a0, a1);
-          add2(s2, s3, s2, s3, b0, b1);
-          w[i / 2] = pack2<T>(a0, a1);
-          w[i / 2 + 1] = pack2<T>(b0, b1);
+          for (int i = 0; i < 32; i += 4) {
+            float a0 = __uint_as_float(x[c][i]), a1 = __uint_as_float(x[c][i + 1]);
+            float b0 = __uint_as_float(x[c][i + 2]), b1 = __uint_as_float(x[c][i + 3]);
+            fma2(a0, a1, a0, a1, sl2, sl2, shift, shift);
+            fma2(b0, b1, b0, b1, sl2, sl2, shift, shift);
+            a0 = ex2(a0);
+            a1 = ex2(a1);
+            if (decltype(poly)::value && i % 8 == 4) {
+              exp2_poly2(b0, b1);
+            } else {
+              b0 = ex2(b0);
+              b1 = ex2(b1);
+            }
+            add2(s0, s1, s0, s1, a0, a1);
+            add2(s2, s3, s2, s3, b0, b1);
+            w[i / 2] = pack2<T>(a0, a1);
+            w[i / 2 + 1] = pack2<T>(b0, b1);
+          }
+          tmem_st16(w_at + 16 * c, w);
+          if (c & 1) {  // half of the weights: their product can start
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_p(t, c >> 1));
+          }
         }
-        tmem_st16(s_at + 16 * c, w);
-      }
+      };
+      // A quarter of the exponentials by polynomial, but not where masked
+      // places must give exactly 0.
+      if (masked)
+        weights(std::false_type{});
+      else
+        weights(std::true_type{});
       sum += (s0 + s1) + (s2 + s3);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_p(t));
     }
-    if (ok && my_steps > 0) ok = mbar_wait(bar_o(t), 0, ab, p.status);
+    if (ok && my_steps > 0) ok = mbar_wait(bar_pv(t), (my_steps - 1) & 1, ab, p.status);
     if (ok) {
       tc_fence_after();
       const bool split = p.max_pieces > 1;
@@ -311,7 +370,7 @@ packed_forward_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_co
       const long long part_row = ((long long)blockIdx.z * p.total_q + i) * p.hq + head;
       // a row that saw no key: zeros and -inf
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      const float lse = sum == 0.f ? -INFINITY : fmaf(ref, p.scale, log2f(sum) * kLn2);
+      const float lse = sum == 0.f ? -INFINITY : fmaf(ref, p.scale, (log2f(sum) - kLift) * kLn2);
       bool finite = fabsf(sum) < INFINITY;
       constexpr int W = D < 32 ? D : 32;
 #pragma unroll

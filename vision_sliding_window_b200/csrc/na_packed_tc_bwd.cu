@@ -60,14 +60,14 @@ struct Bars {
   NA_DEVICE void init(int full_count) const {
     mbar_init(kept(), 1);
     mbar_init(tail(), 1);
-    mbar_init(done(), 1);
+    mbar_init(done(), 2);  // both MMA warps'
     mbar_init(s(), 1);
     mbar_init(dp(), 1);
     mbar_init(p_ready(), 8);
     mbar_init(ds_ready(), 8);
     for (int i = 0; i < stages; ++i) {
       mbar_init(full(i), full_count);
-      mbar_init(empty(i), 1);
+      mbar_init(empty(i), 2);
     }
     mbar_init_fence();
   }
@@ -220,39 +220,43 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         __syncwarp();
         if (lane == 0) mbar_arrive(bar.full(i));
       }
-    } else if (warp == 1 && n > 0) {
+    } else if ((warp == 1 || warp == 3) && n > 0) {
       // -------------------------------------------------------------- MMAs
-      if (lane == 0) {
-        bool ok = mbar_wait(bar.kept(), 0, ab, p.status) && mbar_wait(bar.full(0), 0, ab, p.status);
-        if (ok) {
+      // One warp for S^T and dV, one for dP^T and dK: each runs its two in
+      // turn, and while one looks at its barriers the tensor pipe has the
+      // other's.  The whole warp walks the steps, which keeps what the operands
+      // are made of in uniform registers, and one lane issues.
+      const bool first_warp = warp == 1;
+      const uint32_t at = first_warp ? s_at : dp_at, to = first_warp ? dv_at : dk_at;
+      const uint32_t kept = first_warp ? k_tile : v_tile;
+      const uint32_t ready = first_warp ? bar.p_ready() : bar.ds_ready(), made = first_warp ? bar.s() : bar.dp();
+      // S^T is made of a row tile's Q and dV summed with its dO; dP^T and dK the other way round
+      auto with = [&](int i) { return first_warp ? q_tile(i) : o_tile(i); };
+      auto sums = [&](int i) { return first_warp ? o_tile(i) : q_tile(i); };
+      bool ok = mbar_wait(bar.kept(), 0, ab, p.status) && mbar_wait(bar.full(0), 0, ab, p.status);
+      if (__all_sync(0xffffffffu, ok)) {
+        tc_fence_after();
+        if (elect_one()) {
+          mma_rows_by_rows<D, BF16>(at, kept, with(0));
+          mma_commit(made);
+        }
+        for (int i = 0; i < n; ++i) {
+          ok = i + 1 >= n || mbar_wait(bar.full(i + 1), ((i + 1) / C::STAGES) & 1, ab, p.status);
+          ok = ok && mbar_wait(ready, i & 1, ab, p.status);
+          if (!__all_sync(0xffffffffu, ok)) break;
           tc_fence_after();
-          mma_rows_by_rows<D, BF16>(s_at, k_tile, q_tile(0));
-          mma_commit(bar.s());
-          mma_rows_by_rows<D, BF16>(dp_at, v_tile, o_tile(0));
-          mma_commit(bar.dp());
-          for (int i = 0; i < n; ++i) {
-            if (i + 1 < n && !mbar_wait(bar.full(i + 1), ((i + 1) / C::STAGES) & 1, ab, p.status)) break;
-            if (!mbar_wait(bar.p_ready(), i & 1, ab, p.status)) break;
-            tc_fence_after();
-            // the halves of P^T lie 64 columns apart
-            mma_weights_by_tile<D, BF16, 64>(dv_at, s_at, o_tile(i), i > 0);
-            if (i + 1 < n) {
-              mma_rows_by_rows<D, BF16>(s_at, k_tile, q_tile(i + 1));
-              mma_commit(bar.s());
-            }
-            if (!mbar_wait(bar.ds_ready(), i & 1, ab, p.status)) break;
-            tc_fence_after();
-            mma_weights_by_tile<D, BF16, 64>(dk_at, dp_at, q_tile(i), i > 0);
+          if (elect_one()) {
+            mma_weights_by_tile<D, BF16, 64>(to, at, sums(i), i > 0);  // the halves lie 64 columns apart
             mma_commit(bar.empty(i));
             if (i + 1 < n) {
-              mma_rows_by_rows<D, BF16>(dp_at, v_tile, o_tile(i + 1));
-              mma_commit(bar.dp());
+              mma_rows_by_rows<D, BF16>(at, kept, with(i + 1));
+              mma_commit(made);
             }
           }
         }
-        mma_commit(bar.done());
-        mbar_wait_settle(bar.done(), 0);
       }
+      if (elect_one()) mma_commit(bar.done());
+      mbar_wait_settle(bar.done(), 0);
       __syncwarp();
     }
   } else {
@@ -521,36 +525,48 @@ packed_dq_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
         if (tail_used) mbar_wait_settle(bar.tail(), 0);
         for (int u = max(0, i - C::STAGES); u < i; ++u) mbar_wait_settle(bar.full(u), (u / C::STAGES) & 1);
       }
-    } else if (warp == 1 && n > 0) {
+    } else if ((warp == 1 || warp == 2) && n > 0) {
       // -------------------------------------------------------------- MMAs
-      if (lane == 0) {
-        bool ok = mbar_wait(bar.kept(), 0, ab, p.status) && mbar_wait(bar.full(0), 0, ab, p.status);
-        if (ok) {
-          tc_fence_after();
-          mma_rows_by_rows<D, BF16>(tmem, q_tile, k_tile(0));
-          mma_commit(bar.s());
-          mma_rows_by_rows<D, BF16>(dp_at, o_tile, v_tile(0));
-          mma_commit(bar.dp());
-          for (int i = 0; i < n; ++i) {
-            if (i + 1 < n) {
-              if (!mbar_wait(bar.full(i + 1), ((i + 1) / C::STAGES) & 1, ab, p.status)) break;
-              tc_fence_after();
+      // One warp for S and dQ, one for dP, for the same reason as above.
+      bool ok = mbar_wait(bar.kept(), 0, ab, p.status) && mbar_wait(bar.full(0), 0, ab, p.status);
+      if (__all_sync(0xffffffffu, ok)) {
+        tc_fence_after();
+        if (elect_one()) {
+          if (warp == 1) {
+            mma_rows_by_rows<D, BF16>(tmem, q_tile, k_tile(0));
+            mma_commit(bar.s());
+          } else {
+            mma_rows_by_rows<D, BF16>(dp_at, o_tile, v_tile(0));
+            mma_commit(bar.dp());
+            mma_commit(bar.empty(0));
+          }
+        }
+        for (int i = 0; i < n; ++i) {
+          if (i + 1 < n) {
+            ok = mbar_wait(bar.full(i + 1), ((i + 1) / C::STAGES) & 1, ab, p.status);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            if (warp == 1 && elect_one()) {
               mma_rows_by_rows<D, BF16>(tmem + ((i + 1) & 1) * kTile, q_tile, k_tile(i + 1));
               mma_commit(bar.s());
             }
-            if (!mbar_wait(bar.ds_ready(), i & 1, ab, p.status)) break;
-            tc_fence_after();
-            if (i + 1 < n) {
+          }
+          ok = mbar_wait(bar.ds_ready(), i & 1, ab, p.status);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          tc_fence_after();
+          if (elect_one()) {
+            if (warp == 1) {
+              mma_weights_by_tile<D, BF16, 64>(dq_at, tmem + (i & 1) * kTile, k_tile(i), i > 0);
+              mma_commit(bar.empty(i));
+            } else if (i + 1 < n) {
               mma_rows_by_rows<D, BF16>(dp_at, o_tile, v_tile(i + 1));
               mma_commit(bar.dp());
+              mma_commit(bar.empty(i + 1));
             }
-            mma_weights_by_tile<D, BF16, 64>(dq_at, tmem + (i & 1) * kTile, k_tile(i), i > 0);
-            mma_commit(bar.empty(i));
           }
         }
-        mma_commit(bar.done());
-        mbar_wait_settle(bar.done(), 0);
       }
+      if (elect_one()) mma_commit(bar.done());
+      mbar_wait_settle(bar.done(), 0);
       __syncwarp();
     }
   } else {
