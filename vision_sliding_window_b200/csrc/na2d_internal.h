@@ -93,6 +93,8 @@ struct PackedArgs {
   float2* terms;  // backward: (lse log2 e, out . dout) of every row, [total_q][hq]
   unsigned* status;
 };
+// Row tiles of 128 that a block of the tensor-core forward owns.
+constexpr int packed_row_tiles(int d) { return d > 64 ? 2 : 1; }
 enum { kPathSimt, kPathRows, kPathTc };
 // Sets path, piece_keys and max_pieces (na_packed_simt.cu).
 void packed_plan(PackedArgs* p, na_dtype dt);

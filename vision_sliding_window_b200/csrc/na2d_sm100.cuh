@@ -38,17 +38,6 @@ NA_DEVICE bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Whether the phase has completed, without suspending.
-NA_DEVICE bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 // Waits for the phase of `bar` with the given parity.  Gives up (returns
 // false) when another role of the CTA has given up, or after kWaitLimitNs,
 // in which case it raises the CTA's abort flag and the device status word.

@@ -604,7 +604,7 @@ void packed_plan(PackedArgs* p, na_dtype dt) {
   p->path = dt == NA_F32 || p->group > 128 || p->total_k == 0 ? kPathSimt : few ? kPathRows : kPathTc;
   const long long row_bytes = (long long)p->total_q * p->hq * (p->d + 1) * 4;
   if (p->path == kPathTc) {
-    const int per = 2 * (128 / p->group);
+    const int per = packed_row_tiles(p->d) * (128 / p->group);
     const long long tiles = part_numbers(p->nseq, p->total_q, 1, per) * p->hk;
     long long pieces = kSms / tiles;
     if (pieces > p->total_k / p->nseq / 512) pieces = p->total_k / p->nseq / 512;

@@ -1,8 +1,8 @@
 // na_packed_tc.cu -- forward of the packed attention on the tensor cores, fp16
 // and bf16.
 //
-// A block owns two row tiles (A and B) of one key head and walks the keys they
-// see in tiles of 128:
+// A block owns two row tiles (A and B; one where d <= 64, with two blocks an
+// SM) of one key head and walks the keys they see in tiles of 128:
 //
 //   S_t = Q_t K_j^T  ->  P_t = 2^(S_t scale log2e - ref) in 16 bits
 //   ->  O_t += P_t V_j                        (S, P and O in tensor memory)
@@ -10,9 +10,8 @@
 // with one softmax warpgroup a tile, a thread a row.  A softmax takes S into
 // registers at once, and the next S is made while it works, so that a tile's
 // chain is its softmax alone and the products hide behind it.  That needs P in
-// columns of its own; at d = 128 tensor memory then has room for one S, which
-// the tiles use in turn (each holds it for its product and the load, about 0.8
-// of 2 thousand cycles).  With P over S, softmax and products of a tile took
+// columns of its own; tensor memory then has room for one S, which two tiles
+// use in turn (each holds it for its product and the load).  With P over S, softmax and products of a tile took
 // turns: 3.3 thousand cycles a step where the tensor pipe needs 2.0.
 //
 // O is rescaled only when a row's maximum has grown by 2^8 over its reference:
@@ -33,32 +32,36 @@ using namespace packed;
 
 template <int D> struct Fwd {
   using G = Geo<D>;
-  static constexpr int SLOTS = D == 128 ? 4 : 8;  // ring of K and V tiles, in the order they are used
+  static constexpr int TILES = packed_row_tiles(D);
+  static constexpr int SLOTS = 4;  // ring of K and V tiles, in the order they are used
   static constexpr int Q_OFF = 0;
-  static constexpr int RING_OFF = 2 * G::TILE_BYTES;
+  static constexpr int RING_OFF = TILES * G::TILE_BYTES;
   static constexpr int BAR_OFF = RING_OFF + SLOTS * G::TILE_BYTES;
   static constexpr int SMEM = BAR_OFF + 256 + 1024;
-  // one block an SM, as it holds all of tensor memory
-  static constexpr int SMEM_ASKED = SMEM > 116 * 1024 ? SMEM : 116 * 1024;
-  static_assert(SMEM <= kMaxSmem, "fits");
-  static constexpr int THREADS = 384;
-  static constexpr int REGS_CTRL = 72, REGS_SOFTMAX = 216;
-  // tensor memory: one or two S of 128 columns, P_t of 64, O_t of d
-  static constexpr int S_BUFS = D == 128 ? 1 : 2;
-  static constexpr int P_COL = S_BUFS * kTile, O_COL = P_COL + 2 * 64;
-  static_assert(O_COL + 2 * D <= 512, "fits");
+  // As many blocks an SM as share tensor memory: one of two tiles, or two of
+  // one tile, whose starts and ends then overlap the other's work.
+  static constexpr int BLOCKS = TILES == 2 ? 1 : 2;
+  static constexpr int SMEM_LEAST = BLOCKS == 1 ? 116 * 1024 : 78 * 1024;
+  static constexpr int SMEM_ASKED = SMEM > SMEM_LEAST ? SMEM : SMEM_LEAST;
+  static_assert(SMEM_ASKED * BLOCKS <= kMaxSmem, "fits");
+  static constexpr int THREADS = 128 + 128 * TILES;
+  static constexpr int REGS_CTRL = TILES == 2 ? 72 : 40, REGS_SOFTMAX = TILES == 2 ? 216 : 208;
+  // tensor memory: S of 128 columns, P_t of 64, O_t of d
+  static constexpr int P_COL = kTile, O_COL = P_COL + TILES * 64;
+  static constexpr int TMEM = 512 / BLOCKS;
+  static_assert(O_COL + TILES * D <= TMEM, "fits");
 };
 
 constexpr float kSlack = 8.f;  // log2 of how far a maximum may pass its reference
 
 template <typename T, int D>
-__global__ void __launch_bounds__(Fwd<D>::THREADS, 1)
+__global__ void __launch_bounds__(Fwd<D>::THREADS, Fwd<D>::BLOCKS)
 packed_forward_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                          const __grid_constant__ CUtensorMap mv, const PackedArgs p) {
   using C = Fwd<D>;
   using G = Geo<D>;
   constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value;
-  constexpr int SLOTS = C::SLOTS;
+  constexpr int SLOTS = C::SLOTS, TILES = C::TILES;
   extern __shared__ uint8_t raw[];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
@@ -69,13 +72,13 @@ packed_forward_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_co
   const int kh = blockIdx.y;
   int s;
   long long idx;
-  find_part_warp(p.cu_q, p.nseq, p.total_q, 1, 2 * P, blockIdx.x, &s, &idx);
+  find_part_warp(p.cu_q, p.nseq, p.total_q, 1, TILES * P, blockIdx.x, &s, &idx);
   const Span sp = span_of(p, s);
   // the last rows, which see the most keys, first: the short blocks fill the
   // gaps at the end
-  const long long part = (sp.nq + 2 * P - 1) / (2 * P) - 1 - idx;
+  const long long part = (sp.nq + TILES * P - 1) / (TILES * P) - 1 - idx;
   if (idx < 0 || part < 0) return;
-  const int pos0 = (int)part * 2 * P;
+  const int pos0 = (int)part * TILES * P;
   int piece0 = 0, piece1 = sp.nk;
   if (p.max_pieces > 1) {
     const int len = piece_length(p, sp);
@@ -84,21 +87,17 @@ packed_forward_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_co
     if (blockIdx.z > 0 && piece0 >= piece1) return;
   }
   // tile t: positions [pos0 + t P, ...), key tiles 0 .. steps[t] from kb on
-  int kb = 0, steps[2], ends[2];
+  int kb = 0, steps[2] = {0, 0};
   {
     int lo, hi, unused;
     visible(p, sp, pos0, &lo, &unused);
     kb = max(lo, piece0);
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < TILES; ++t) {
       const int last = min(pos0 + (t + 1) * P, sp.nq) - 1;
-      if (last < pos0 + t * P) {
-        ends[t] = kb;
-      } else {
-        visible(p, sp, last, &unused, &hi);
-        ends[t] = max(min(hi, piece1), kb);
-      }
-      steps[t] = (ends[t] - kb + kTile - 1) / kTile;
+      if (last < pos0 + t * P) continue;
+      visible(p, sp, last, &unused, &hi);
+      steps[t] = (max(min(hi, piece1), kb) - kb + kTile - 1) / kTile;
     }
   }
   const int n = max(steps[0], steps[1]);
@@ -114,7 +113,7 @@ packed_forward_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_co
   auto bar_s = [&](int t) { return bars + 8 + (2 * SLOTS + t) * 8; };       // S_t is made
   auto bar_pv = [&](int t) { return bars + 8 + (2 * SLOTS + 2 + t) * 8; };  // O_t has P_t V
   auto bar_p = [&](int t, int half) { return bars + 8 + (2 * SLOTS + 4 + 2 * t + half) * 8; };
-  auto bar_free = [&](int b) { return bars + 8 + (2 * SLOTS + 8 + b) * 8; };  // an S is in registers
+  const uint32_t bar_free = bars + 8 + (2 * SLOTS + 8) * 8;  // S is in registers
   const uint32_t bar_tail = bars + 8 + (2 * SLOTS + 10) * 8, bar_done0 = bar_tail + 8;
   auto bar_done = [&](int w) { return bar_done0 + w * 8; };
   if (threadIdx.x == 0) {
@@ -129,14 +128,15 @@ packed_forward_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_co
       mbar_init(bar_p(t, 0), 4);
       mbar_init(bar_p(t, 1), 4);
       mbar_init(bar_pv(t), 1);
-      mbar_init(bar_free(t), 4);
+
     }
+    mbar_init(bar_free, 4);
     mbar_init(bar_tail, 1);
     mbar_init(bar_done(0), 1);
     mbar_init(bar_done(1), 1);
     mbar_init_fence();
   }
-  if (warp == 1) tmem_alloc(smem_addr(&tmem_slot), 512);
+  if (warp == 1) tmem_alloc(smem_addr(&tmem_slot), C::TMEM);
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&mq);
     tma_prefetch_desc(&mk);
@@ -157,8 +157,8 @@ packed_forward_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_co
       // ------------------------------------------------------------- loads
       // The ring holds K_0, V_0, K_1, V_1, ...
       if (lane == 0) {
-        mbar_expect_tx(bar_q(), (uint32_t)(2 * P * p.group * D * 2));
-        for (int t = 0; t < 2; ++t) load_row_tile<D>(q_tile(t), &mq, bar_q(), kh, sp.q0 + pos0 + t * P);
+        mbar_expect_tx(bar_q(), (uint32_t)(TILES * P * p.group * D * 2));
+        for (int t = 0; t < TILES; ++t) load_row_tile<D>(q_tile(t), &mq, bar_q(), kh, sp.q0 + pos0 + t * P);
       }
       bool tail_used = false;
       int i = 0;
@@ -193,18 +193,18 @@ packed_forward_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_co
       // The whole warp walks the steps, which keeps what the operands are made
       // of in uniform registers, and one lane issues.
       bool ok = mbar_wait(bar_q(), 0, ab, p.status);
-      int used[2] = {0, 0};  // of each S
+      int made = 0;
       for (int j = 0; j < n; ++j) {
         ok = ok && mbar_wait(bar_full(2 * j), (2 * j / SLOTS) & 1, ab, p.status);
-        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) {
           if (j >= steps[t]) continue;
-          const int b = C::S_BUFS == 1 ? 0 : t;
-          if (used[b] > 0) ok = ok && mbar_wait(bar_free(b), (used[b] - 1) & 1, ab, p.status);
+          if (made > 0) ok = ok && mbar_wait(bar_free, (made - 1) & 1, ab, p.status);
           if (!(ok = __all_sync(0xffffffffu, ok))) break;
-          ++used[b];
+          ++made;
           tc_fence_after();
           if (elect_one()) {
-            mma_rows_by_rows<D, BF16>(tmem + b * kTile, q_tile(t), slot(2 * j));
+            mma_rows_by_rows<D, BF16>(tmem, q_tile(t), slot(2 * j));
             mma_commit(bar_s(t));
           }
         }
@@ -220,7 +220,8 @@ packed_forward_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_co
       bool ok = true;
       for (int j = 0; j < n && ok; ++j) {
         ok = mbar_wait(bar_full(2 * j + 1), ((2 * j + 1) / SLOTS) & 1, ab, p.status);
-        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) {
           if (j >= steps[t]) continue;
           const uint32_t o = tmem + C::O_COL + t * D, w = tmem + C::P_COL + t * 64;
           ok = ok && mbar_wait(bar_p(t, 0), j & 1, ab, p.status);
@@ -246,8 +247,7 @@ packed_forward_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_co
     // ---------------------------------------------------- softmax, epilogue
     const int t = (warp >> 2) - 1, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const int buf = C::S_BUFS == 1 ? 0 : t;
-    const uint32_t s_at = tmem + lanes + buf * kTile, w_at = tmem + lanes + C::P_COL + t * 64;
+    const uint32_t s_at = tmem + lanes, w_at = tmem + lanes + C::P_COL + t * 64;
     const uint32_t o_at = tmem + lanes + C::O_COL + t * D;
     const int at = row / p.group;  // position in the tile
     const int pos = pos0 + t * P + at;
@@ -272,7 +272,7 @@ packed_forward_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_co
       for (int c = 0; c < 4; ++c) tmem_wait_ld_regs(x[c]);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_free(buf));
+      if (lane == 0) mbar_arrive(bar_free);
       const int k0 = kb + j * kTile;
       const bool masked = k0 < all_lo || k0 + kTile > all_hi;
       if (masked) {
@@ -352,7 +352,7 @@ packed_forward_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_co
           }
         }
       };
-      // A quarter of the exponentials by polynomial, but not where masked
+      // Three eighths of the exponentials by polynomial, but not where masked
       // places must give exactly 0.
       if (masked)
         weights(std::false_type{});
@@ -444,17 +444,17 @@ packed_forward_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_co
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, C::TMEM);
   }
 }
 
 template <typename T, int D> cudaError_t launch(const PackedArgs& p, cudaStream_t st) {
   using C = Fwd<D>;
   constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
-  const long long blocks = part_numbers(p.nseq, p.total_q, 1, 2 * (kTile / p.group));
+  const long long blocks = part_numbers(p.nseq, p.total_q, 1, C::TILES * (kTile / p.group));
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   cudaError_t e = prepare_kernel<packed_forward_tc_kernel<T, D>>(
-      C::SMEM_ASKED, C::THREADS, 128 * C::REGS_CTRL + 256 * C::REGS_SOFTMAX);
+      C::SMEM_ASKED, C::THREADS, 128 * C::REGS_CTRL + 128 * C::TILES * C::REGS_SOFTMAX);
   if (e != cudaSuccess) return e;
   CUtensorMap mq, mk, mv;
   if (!row_map(&mq, p.q, p, bf16) || !key_map(&mk, p.k, p, bf16) || !key_map(&mv, p.v, p, bf16))
