@@ -66,10 +66,11 @@ struct NormArgs {
   long long rows, gate_rows;  // gate_rows rows share a row of the gate
   int C, rms, post;
   float eps, scale;
+  unsigned* status;
   int lanes, pieces;  // set by the launchers
   long long chunks, chunk_rows;
 };
-size_t norm_workspace_bytes(long long rows, int C, long long gate_rows);
+size_t norm_workspace_bytes(long long rows, int C, long long gate_rows, na_dtype dt);
 cudaError_t launch_norm_forward(const NormArgs& p, na_dtype dt, cudaStream_t st);
 cudaError_t launch_norm_backward(NormArgs p, na_dtype dt, cudaStream_t st);
 

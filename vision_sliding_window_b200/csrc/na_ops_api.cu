@@ -170,13 +170,14 @@ NA_EXPORT na_status na_norm_forward(const void* x, const void* o, const void* po
   p.b = b;
   p.y = y;
   p.h = h;
+  if (status_word(&p.status) != cudaSuccess) return NA_ERR_CUDA;
   return from_cuda(launch_norm_forward(p, dt, (cudaStream_t)stream));
 }
 
 NA_EXPORT size_t na_norm_backward_workspace_bytes(long long rows, int C, long long gates, na_dtype dt) {
   NormArgs p;
   if (check_norm(rows, C, gates, 0, 0, 0.f, 1.f, dt, &p) != NA_OK || rows == 0) return 0;
-  return norm_workspace_bytes(rows, C, p.gate_rows);
+  return norm_workspace_bytes(rows, C, p.gate_rows, dt);
 }
 
 NA_EXPORT na_status na_norm_backward(const void* y, const void* o, const void* post_w, const void* post_b,
@@ -196,7 +197,7 @@ NA_EXPORT na_status na_norm_backward(const void* y, const void* o, const void* p
   for (const void* ptr : {o, post_w, post_b, gate, w, dy, dh, (const void*)d_o, (const void*)dw, (const void*)db,
                           (const void*)dpost_w, (const void*)dpost_b, (const void*)dgate})
     if (bad(ptr, false)) return NA_ERR_INVALID_ARG;
-  if (workspace_bytes < norm_workspace_bytes(rows, C, p.gate_rows)) return NA_ERR_INVALID_ARG;
+  if (workspace_bytes < norm_workspace_bytes(rows, C, p.gate_rows, dt)) return NA_ERR_INVALID_ARG;
   p.x = y;
   p.o = o;
   p.pw = post_w;
@@ -213,6 +214,7 @@ NA_EXPORT na_status na_norm_backward(const void* y, const void* o, const void* p
   p.dpb = dpost_b;
   p.dgate = dgate;
   p.partial = (float*)workspace;
+  if (status_word(&p.status) != cudaSuccess) return NA_ERR_CUDA;
   return from_cuda(launch_norm_backward(p, dt, (cudaStream_t)stream));
 }
 

@@ -8,6 +8,7 @@ succeeds but every call raises -- there is no other implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import NamedTuple
@@ -288,16 +289,17 @@ def forward_nd(q, k, v, rpb, ks, dilation=None, out=None):
 
 def _need_all(like, dtype, **tensors):
     """_need for every tensor that is given, and that it lies on the device of `like`."""
+    where = like.get_device()
     for name, t in tensors.items():
         if t is None:
             continue
-        _need(t, name, dtype)
-        if t.device != like.device:
+        if (dtype is not None and t.dtype is not dtype) or not t.is_contiguous() or t.get_device() != where:
+            _need(t, name, dtype)
             raise ValueError(f"{name} is on {t.device}, not on {like.device}")
 
 
 def _need_shape(t, name, shape):
-    if t is not None and tuple(t.shape) != tuple(shape):
+    if t is not None and t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
@@ -307,6 +309,24 @@ def _workspace(given, need: int, like):
         return (torch.empty(need, dtype=torch.uint8, device=like.device), need) if need else (None, 0)
     _need_all(like, None, workspace=given)
     return given, given.numel() * given.element_size()
+
+
+def _enqueue(like, name, *args):
+    """Calls the library on the device of `like` and the current stream there; a tensor stands for its address."""
+    where = like.get_device()
+    call = getattr(_lib or load_library(), name)
+    args = [a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args]
+    if where == torch.cuda.current_device():
+        _check(call(*args, torch.cuda.current_stream(where).cuda_stream), name)
+    else:
+        with torch.cuda.device(where):
+            _check(call(*args, torch.cuda.current_stream(where).cuda_stream), name)
+
+
+@functools.lru_cache(maxsize=4096)
+def _bytes_for(name, *sizes) -> int:
+    """A workspace size, which depends on the sizes alone."""
+    return int(getattr(load_library(), name)(*sizes))
 
 
 def _packed_dims(q, k, v, cu_q, cu_k, len_k):
@@ -347,13 +367,10 @@ def packed_forward(q, k, v, cu_q, cu_k, len_k=None, causal: bool = False, window
     _need_all(q, torch.float32, lse=lse)
     _need_shape(out, "out", q.shape)
     _need_shape(lse, "lse", (hq, tq))
-    lib, dt = load_library(), _DT[q.dtype]
-    with torch.cuda.device(q.device):
-        workspace, size = _workspace(workspace, int(lib.na_packed_workspace_bytes(*dims, dt)), q)
-        _check(lib.na_packed_forward(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_q), _ptr(cu_k), _ptr(len_k), _ptr(out),
-                                     _ptr(lse), _ptr(workspace), size, *dims, int(causal), int(window),
-                                     d ** -0.5 if scale is None else float(scale), dt, _stream(q)),
-               "na_packed_forward")
+    dt = _DT[q.dtype]
+    workspace, size = _workspace(workspace, _bytes_for("na_packed_workspace_bytes", *dims, dt), q)
+    _enqueue(q, "na_packed_forward", q, k, v, cu_q, cu_k, len_k, out, lse, workspace, size, *dims, int(causal),
+             int(window), d ** -0.5 if scale is None else float(scale), dt)
     return out, lse
 
 
@@ -374,13 +391,10 @@ def packed_backward(q, k, v, out, lse, dout, cu_q, cu_k, causal: bool = False, w
     _need_shape(dq, "dq", q.shape)
     _need_shape(dk, "dk", k.shape)
     _need_shape(dv, "dv", v.shape)
-    lib, dt = load_library(), _DT[q.dtype]
-    with torch.cuda.device(q.device):
-        workspace, size = _workspace(workspace, int(lib.na_packed_backward_workspace_bytes(*dims, dt)), q)
-        _check(lib.na_packed_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout), _ptr(cu_q),
-                                      _ptr(cu_k), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), size, *dims,
-                                      int(causal), int(window), d ** -0.5 if scale is None else float(scale), dt,
-                                      _stream(q)), "na_packed_backward")
+    dt = _DT[q.dtype]
+    workspace, size = _workspace(workspace, _bytes_for("na_packed_backward_workspace_bytes", *dims, dt), q)
+    _enqueue(q, "na_packed_backward", q, k, v, out, lse, dout, cu_q, cu_k, dq, dk, dv, workspace, size, *dims,
+             int(causal), int(window), d ** -0.5 if scale is None else float(scale), dt)
     return dq, dk, dv
 
 
@@ -427,11 +441,8 @@ def norm_forward(x, w=None, b=None, o=None, post: bool = False, post_w=None, pos
     _need_all(x, x.dtype, y=y, h=h)
     _need_shape(y, "y", x.shape)
     _need_shape(h, "h", x.shape)
-    with torch.cuda.device(x.device):
-        _check(load_library().na_norm_forward(_ptr(x), _ptr(o), _ptr(post_w), _ptr(post_b), _ptr(gate), _ptr(w),
-                                              _ptr(b), _ptr(y), _ptr(h), rows, C, gates, int(rms), int(post),
-                                              float(eps), float(scale), _DT[x.dtype], _stream(x)),
-               "na_norm_forward")
+    _enqueue(x, "na_norm_forward", x, o, post_w, post_b, gate, w, b, y, h, rows, C, gates, int(rms), int(post),
+             float(eps), float(scale), _DT[x.dtype])
     return (x if o is None else y), h
 
 
@@ -462,13 +473,10 @@ def norm_backward(y, dh, dy=None, w=None, b=None, o=None, post: bool = False, po
         return None if t is None else torch.empty(t.shape, device=y.device, dtype=dtype)
 
     g = NormGrads(torch.empty_like(y), like(o, y.dtype), like(w), like(b), like(post_w), like(post_b), like(gate))
-    lib, dt = load_library(), _DT[y.dtype]
-    with torch.cuda.device(y.device):
-        workspace, size = _workspace(workspace, int(lib.na_norm_backward_workspace_bytes(rows, C, gates, dt)), y)
-        _check(lib.na_norm_backward(_ptr(y), _ptr(o), _ptr(post_w), _ptr(post_b), _ptr(gate), _ptr(w), _ptr(dy),
-                                    _ptr(dh), _ptr(g.dx), _ptr(g.do), _ptr(g.dw), _ptr(g.db), _ptr(g.dpost_w),
-                                    _ptr(g.dpost_b), _ptr(g.dgate), _ptr(workspace), size, rows, C, gates, int(rms),
-                                    int(post), float(eps), float(scale), dt, _stream(y)), "na_norm_backward")
+    dt = _DT[y.dtype]
+    workspace, size = _workspace(workspace, _bytes_for("na_norm_backward_workspace_bytes", rows, C, gates, dt), y)
+    _enqueue(y, "na_norm_backward", y, o, post_w, post_b, gate, w, dy, dh, g.dx, g.do, g.dw, g.db, g.dpost_w,
+             g.dpost_b, g.dgate, workspace, size, rows, C, gates, int(rms), int(post), float(eps), float(scale), dt)
     return g
 
 
@@ -491,13 +499,10 @@ def layer_forward(x, w, b, wqkv, bqkv, wo, bo, rpb, heads: int, ksize: int, gate
     y = torch.empty_like(x) if y is None else y
     _need_all(x, x.dtype, y=y)
     _need_shape(y, "y", x.shape)
-    lib, dt, dims = load_library(), _DT[x.dtype], (B, H, W, heads, C // heads, ksize)
-    with torch.cuda.device(x.device):
-        workspace, size = _workspace(workspace, int(lib.na2d_layer_workspace_bytes(*dims, dt)), x)
-        _check(lib.na2d_layer_forward(_ptr(x), _ptr(w), _ptr(b), _ptr(wqkv), _ptr(bqkv), _ptr(wo), _ptr(bo),
-                                      _ptr(rpb), _ptr(post_w), _ptr(post_b), _ptr(gate), _ptr(y), _ptr(workspace),
-                                      size, *dims, gates, int(rms), int(post), float(eps), float(scale), dt,
-                                      _stream(x)), "na2d_layer_forward")
+    dt, dims = _DT[x.dtype], (B, H, W, heads, C // heads, ksize)
+    workspace, size = _workspace(workspace, _bytes_for("na2d_layer_workspace_bytes", *dims, dt), x)
+    _enqueue(x, "na2d_layer_forward", x, w, b, wqkv, bqkv, wo, bo, rpb, post_w, post_b, gate, y, workspace, size,
+             *dims, gates, int(rms), int(post), float(eps), float(scale), dt)
     return y
 
 
