@@ -584,8 +584,8 @@ NA_DEVICE void wide_stats(float (&v)[K][NV][VEC], const bool (&in)[NV], float in
   for (int k = 0; k < K; ++k) rstd[k] = rsqrtf(s[k] * inv + eps);
 }
 
-template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(512, 1) norm_forward_wide_kernel(NormArgs p, int stages) {
+template <typename T, int VEC, int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1) norm_forward_wide_kernel(NormArgs p, int stages) {
   using namespace sm100;
   extern __shared__ __align__(128) uint8_t ring_data[];
   __shared__ float scratch[2][2][32];
@@ -923,10 +923,10 @@ cudaError_t forward_one(const NormArgs& p, int lanes, int block, cudaStream_t st
   return cudaGetLastError();
 }
 
-template <typename T, int VEC, int NV>
+template <typename T, int VEC, int NV, int THREADS>
 cudaError_t forward_wide(const NormArgs& p, int block, cudaStream_t st) {
-  auto kern = norm_forward_wide_kernel<T, VEC, NV>;
-  const int per_sm = block <= 256 ? 2 : 1;  // registers leave room for 512 threads
+  auto kern = norm_forward_wide_kernel<T, VEC, NV, THREADS>;
+  const int per_sm = THREADS == 256 ? (block <= 128 ? 6 : 3) : 1;  // as many as registers leave room for
   const size_t stage = (size_t)p.C * sizeof(T) * (p.o ? 2 : 1);
   const int stages = ring_stages(stage, per_sm);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 216 * 1024);
@@ -943,7 +943,11 @@ template <typename T, int VEC> cudaError_t forward_vec(NormArgs p, cudaStream_t 
     // 16 columns a thread: each warp's share of reductions and addresses is
     // most of its instructions with 8, and registers spill with 32
     if constexpr (VEC * sizeof(T) == 16)  // rows that bulk copies can take
-      return forward_wide<T, VEC, 16 / VEC>(p, block_of(pl.block, 16 / VEC), st);
+    {
+      const int block = block_of(pl.block, 16 / VEC);
+      return block <= 256 ? forward_wide<T, VEC, 16 / VEC, 256>(p, block, st)
+                          : forward_wide<T, VEC, 16 / VEC, 512>(p, block, st);
+    }
     else
       return forward_one<T, VEC, 8 / VEC, true>(p, 0, block_of(pl.block, 8 / VEC), st);
   }

@@ -291,9 +291,8 @@ def _need_all(like, dtype, **tensors):
     """_need for every tensor that is given, and that it lies on the device of `like`."""
     where = like.get_device()
     for name, t in tensors.items():
-        if t is None:
-            continue
-        if (dtype is not None and t.dtype is not dtype) or not t.is_contiguous() or t.get_device() != where:
+        if t is not None and not (t.get_device() == where and (dtype is None or t.dtype is dtype)
+                                  and t.is_contiguous()):
             _need(t, name, dtype)
             raise ValueError(f"{name} is on {t.device}, not on {like.device}")
 
@@ -311,16 +310,27 @@ def _workspace(given, need: int, like):
     return given, given.numel() * given.element_size()
 
 
-def _enqueue(like, name, *args):
-    """Calls the library on the device of `like` and the current stream there; a tensor stands for its address."""
+def _enqueue(like, name, tensors, *numbers):
+    """Calls the library with the tensors' addresses (None: NULL) and the numbers, on the device of `like` and the
+    current stream there."""
     where = like.get_device()
     call = getattr(_lib or load_library(), name)
-    args = [a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args]
+    at = [None if t is None else t.data_ptr() for t in tensors]
     if where == torch.cuda.current_device():
-        _check(call(*args, torch.cuda.current_stream(where).cuda_stream), name)
+        status = call(*at, *numbers, _raw_stream(where))
     else:
         with torch.cuda.device(where):
-            _check(call(*args, torch.cuda.current_stream(where).cuda_stream), name)
+            status = call(*at, *numbers, _raw_stream(where))
+    if status != NA_OK:
+        raise NA2DError(status, name)
+
+
+def _raw_stream(device: int) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):  # the same without building a Stream object
+    _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 @functools.lru_cache(maxsize=4096)
@@ -369,7 +379,7 @@ def packed_forward(q, k, v, cu_q, cu_k, len_k=None, causal: bool = False, window
     _need_shape(lse, "lse", (hq, tq))
     dt = _DT[q.dtype]
     workspace, size = _workspace(workspace, _bytes_for("na_packed_workspace_bytes", *dims, dt), q)
-    _enqueue(q, "na_packed_forward", q, k, v, cu_q, cu_k, len_k, out, lse, workspace, size, *dims, int(causal),
+    _enqueue(q, "na_packed_forward", (q, k, v, cu_q, cu_k, len_k, out, lse, workspace), size, *dims, int(causal),
              int(window), d ** -0.5 if scale is None else float(scale), dt)
     return out, lse
 
@@ -393,7 +403,7 @@ def packed_backward(q, k, v, out, lse, dout, cu_q, cu_k, causal: bool = False, w
     _need_shape(dv, "dv", v.shape)
     dt = _DT[q.dtype]
     workspace, size = _workspace(workspace, _bytes_for("na_packed_backward_workspace_bytes", *dims, dt), q)
-    _enqueue(q, "na_packed_backward", q, k, v, out, lse, dout, cu_q, cu_k, dq, dk, dv, workspace, size, *dims,
+    _enqueue(q, "na_packed_backward", (q, k, v, out, lse, dout, cu_q, cu_k, dq, dk, dv, workspace), size, *dims,
              int(causal), int(window), d ** -0.5 if scale is None else float(scale), dt)
     return dq, dk, dv
 
@@ -441,7 +451,7 @@ def norm_forward(x, w=None, b=None, o=None, post: bool = False, post_w=None, pos
     _need_all(x, x.dtype, y=y, h=h)
     _need_shape(y, "y", x.shape)
     _need_shape(h, "h", x.shape)
-    _enqueue(x, "na_norm_forward", x, o, post_w, post_b, gate, w, b, y, h, rows, C, gates, int(rms), int(post),
+    _enqueue(x, "na_norm_forward", (x, o, post_w, post_b, gate, w, b, y, h), rows, C, gates, int(rms), int(post),
              float(eps), float(scale), _DT[x.dtype])
     return (x if o is None else y), h
 
@@ -469,14 +479,20 @@ def norm_backward(y, dh, dy=None, w=None, b=None, o=None, post: bool = False, po
     _need_shape(dh, "dh", y.shape)
     _need_shape(dy, "dy", y.shape)
 
-    def like(t, dtype=torch.float32):
-        return None if t is None else torch.empty(t.shape, device=y.device, dtype=dtype)
-
-    g = NormGrads(torch.empty_like(y), like(o, y.dtype), like(w), like(b), like(post_w), like(post_b), like(gate))
+    sums = (w, b, post_w, post_b)
+    given = [t is not None for t in sums]
+    # one allocation for the gradients of all weights of a channel each, every
+    # one aligned as the library wants it
+    pad = -(-C // 4) * 4
+    rest = iter(torch.empty((sum(given), pad), device=y.device, dtype=torch.float32)[:, :C].unbind() if any(given)
+                else ())
+    g = NormGrads(torch.empty_like(y), None if o is None else torch.empty_like(y),
+                  *(next(rest) if there else None for there in given),
+                  None if gate is None else torch.empty(gate.shape, device=y.device, dtype=torch.float32))
     dt = _DT[y.dtype]
     workspace, size = _workspace(workspace, _bytes_for("na_norm_backward_workspace_bytes", rows, C, gates, dt), y)
-    _enqueue(y, "na_norm_backward", y, o, post_w, post_b, gate, w, dy, dh, g.dx, g.do, g.dw, g.db, g.dpost_w,
-             g.dpost_b, g.dgate, workspace, size, rows, C, gates, int(rms), int(post), float(eps), float(scale), dt)
+    _enqueue(y, "na_norm_backward", (y, o, post_w, post_b, gate, w, dy, dh, *g, workspace), size, rows, C, gates,
+             int(rms), int(post), float(eps), float(scale), dt)
     return g
 
 
@@ -501,7 +517,7 @@ def layer_forward(x, w, b, wqkv, bqkv, wo, bo, rpb, heads: int, ksize: int, gate
     _need_shape(y, "y", x.shape)
     dt, dims = _DT[x.dtype], (B, H, W, heads, C // heads, ksize)
     workspace, size = _workspace(workspace, _bytes_for("na2d_layer_workspace_bytes", *dims, dt), x)
-    _enqueue(x, "na2d_layer_forward", x, w, b, wqkv, bqkv, wo, bo, rpb, post_w, post_b, gate, y, workspace, size,
+    _enqueue(x, "na2d_layer_forward", (x, w, b, wqkv, bqkv, wo, bo, rpb, post_w, post_b, gate, y, workspace), size,
              *dims, gates, int(rms), int(post), float(eps), float(scale), dt)
     return y
 
