@@ -249,7 +249,9 @@ na_status na_packed_forward(const void *q, const void *k, const void *v, const i
  *   P_ij = e^(s_ij - lse_i),  dS_ij = P_ij (dout_i . v_j - dout_i . out_i),
  *   dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,  dv_j = sum_i P_ij dout_i,
  *
- * dk and dv summed over the heads of the group too.  Arguments as the
+ * dk and dv summed over the heads of the group too (where a row's keys are few,
+ * sum_j P_ij dout_i . v_j stands for dout_i . out_i, which it equals but for
+ * out's rounding).  Arguments as the
  * forward's; every key slot belongs to the sequence (there is no len_k).
  * dq, dk and dv are written, not added to; rows of no sequence are left as
  * they were.  Each gradient is summed in a fixed order, so a call's results

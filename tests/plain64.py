@@ -75,7 +75,10 @@ def forward(q, k, v, cu_q, cu_k, len_k=None, causal=False, window=0, scale=None)
 
 
 def backward(q, k, v, out, lse, dout, cu_q, cu_k, causal=False, window=0, scale=None):
-    """(dq, dk, dv) from the out and lse given, and the bounds on their errors."""
+    """(dq, dk, dv) from the lse given, and the bounds on their errors.
+
+    dS = P (dP - sum P dP).  The sum equals dout . out, from which it may be taken:
+    out is then off by what forward() bounds, so the sum by that times |dout|."""
     d, hq, group = q.shape[2], q.shape[1], q.shape[1] // k.shape[1]
     scale = d ** -0.5 if scale is None else scale
     u, sub = half_step(q.dtype), (2.0 ** -25 if q.dtype == torch.float16 else 0.0)
@@ -95,10 +98,13 @@ def backward(q, k, v, out, lse, dout, cu_q, cu_k, causal=False, window=0, scale=
             p = (s - l.nan_to_num(neginf=0.0)[:, None]).exp()
             e = e + 4 * F * l.nan_to_num(neginf=0.0).abs()[:, None]
             dp = go @ c.t()
-            delta = (go * out[q0:q0 + lq, h].double()).sum(1, keepdim=True)
+            delta = (p * dp).sum(1, keepdim=True)
             ds = p * (dp - delta)
+            mag = p @ c.abs()
+            out_err = (u + 2 * e + lk * F) * mag + u * out[q0:q0 + lq, h].double().abs() + sub * (keep.double() @ c.abs())
+            delta_err = (go.abs() * out_err).sum(1, keepdim=True)
             # errors of dp and delta (float32 sums) and of the weight
-            ds_err = p * ((d + 4) * F * (go.abs() @ c.abs().t() + (go * out[q0:q0 + lq, h].double()).abs().sum(1, keepdim=True)))
+            ds_err = p * ((d + 4 + lk) * F * (go.abs() @ c.abs().t() + (go.abs() * mag).sum(1, keepdim=True)) + delta_err)
             ds_err = ds_err + ds.abs() * (e + u) + sub * keep
             p_err = p * (e + u) + sub * keep
             dq[q0:q0 + lq, h] = scale * (ds @ b)

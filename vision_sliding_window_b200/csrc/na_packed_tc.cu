@@ -69,10 +69,10 @@ packed_forward_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_co
 
   // ------------------------------------------------------------ what to do
   const int P = kTile / p.group;  // positions of a row tile
-  const int kh = blockIdx.y;
+  const int kh = blockIdx.x % p.hk;  // the heavy tiles of all heads start first
   int s;
   long long idx;
-  find_part_warp(p.cu_q, p.nseq, p.total_q, 1, TILES * P, blockIdx.x, &s, &idx);
+  find_part_warp(p.cu_q, p.nseq, p.total_q, 1, TILES * P, blockIdx.x / p.hk, &s, &idx);
   const Span sp = span_of(p, s);
   // the last rows, which see the most keys, first: the short blocks fill the
   // gaps at the end
@@ -82,9 +82,9 @@ packed_forward_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_co
   int piece0 = 0, piece1 = sp.nk;
   if (p.max_pieces > 1) {
     const int len = piece_length(p, sp);
-    piece0 = (int)min((long long)blockIdx.z * len, (long long)sp.nk);
+    piece0 = (int)min((long long)blockIdx.y * len, (long long)sp.nk);
     piece1 = (int)min((long long)piece0 + len, (long long)sp.nk);
-    if (blockIdx.z > 0 && piece0 >= piece1) return;
+    if (blockIdx.y > 0 && piece0 >= piece1) return;
   }
   // tile t: positions [pos0 + t P, ...), key tiles 0 .. steps[t] from kb on
   int kb = 0, steps[2] = {0, 0};
@@ -367,7 +367,7 @@ packed_forward_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_co
       const long long i = (long long)sp.q0 + pos;
       const int head = kh * p.group + row % p.group;
       const long long out_row = i * p.hq + head;
-      const long long part_row = ((long long)blockIdx.z * p.total_q + i) * p.hq + head;
+      const long long part_row = ((long long)blockIdx.y * p.total_q + i) * p.hq + head;
       // a row that saw no key: zeros and -inf
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       const float lse = sum == 0.f ? -INFINITY : fmaf(ref, p.scale, (log2f(sum) - kLift) * kLn2);
@@ -452,7 +452,7 @@ template <typename T, int D> cudaError_t launch(const PackedArgs& p, cudaStream_
   using C = Fwd<D>;
   constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
   const long long blocks = part_numbers(p.nseq, p.total_q, 1, C::TILES * (kTile / p.group));
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  if (blocks * p.hk > 0x7fffffffLL) return cudaErrorInvalidValue;
   cudaError_t e = prepare_kernel<packed_forward_tc_kernel<T, D>>(
       C::SMEM_ASKED, C::THREADS, 128 * C::REGS_CTRL + 128 * C::TILES * C::REGS_SOFTMAX);
   if (e != cudaSuccess) return e;
@@ -460,7 +460,7 @@ template <typename T, int D> cudaError_t launch(const PackedArgs& p, cudaStream_
   if (!row_map(&mq, p.q, p, bf16) || !key_map(&mk, p.k, p, bf16) || !key_map(&mv, p.v, p, bf16))
     return cudaErrorInvalidValue;
   packed_forward_tc_kernel<T, D>
-      <<<dim3((unsigned)blocks, (unsigned)p.hk, (unsigned)(p.max_pieces > 1 ? p.max_pieces : 1)), C::THREADS,
+      <<<dim3((unsigned)(blocks * p.hk), (unsigned)p.max_pieces), C::THREADS,
          C::SMEM_ASKED, st>>>(mq, mk, mv, p);
   return cudaGetLastError();
 }

@@ -113,6 +113,29 @@ template <int D> NA_DEVICE void zero_rows(uint32_t tile, int from) {
   fence_async_smem();
 }
 
+// One tile of a ring, by a warp: `load` starts the copies of `bytes` to the slot
+// on a barrier.  Of a sequence's last tile, rows `left` to `rows`, which are not
+// the sequence's, are zeroed before the slot counts as full: neither a zero
+// weight nor a zero gradient stops a NaN.  `tail` is a barrier for that copy
+// (two of them, one for each of two rings: it completes when both have landed).
+template <int D, typename F>
+NA_DEVICE bool load_ring_tile(uint32_t slot, uint32_t full, uint32_t tail, int left, int rows, uint32_t bytes,
+                              volatile int* ab, unsigned* status, F load) {
+  const int lane = threadIdx.x & 31;
+  const bool cut = left < rows;
+  if (lane == 0) {
+    mbar_expect_tx(cut ? tail : full, bytes);
+    load(slot, cut ? tail : full);
+  }
+  __syncwarp();
+  if (!cut) return true;
+  if (!mbar_wait(tail, 0, ab, status)) return false;
+  zero_rows<D>(slot, left);
+  __syncwarp();
+  if (lane == 0) mbar_arrive(full);
+  return true;
+}
+
 // 2^x without the special-function unit, which bounds a softmax fed by the
 // tensor cores: x = n + f with n the nearest integer, 2^f by the polynomial of
 // degree 4 that meets it at the five Chebyshev points of [-1/2, 1/2] (off by at

@@ -19,12 +19,18 @@
 // from tensor memory.  The products are issued so that the tensor pipe always
 // has one while a half of the element-wise work runs: dV and the next S^T
 // beside dS^T, dK and the next dP^T beside P^T.  Two warpgroups share a tile,
-// each 64 of its columns, a thread a lane.  Shared-memory reads of the
-// operands bound the first kernel at d = 128 (two products with both operands
-// there and two with one: 1536 of about 2048 cycles of a step, and the
-// copies' writes 512 more).
+// each 64 of its columns, a thread a lane.  The tiles that are walked come
+// through two rings, as Q and dO (K and V) are done with at different times:
+// with both in one ring of two stages at d = 128, a step waited 1.5 of 3.5
+// thousand cycles for its loads.
 //
-// P and dS are rounded to the input type for their products.
+// P and dS are rounded to the input type for their products.  fp16 weights are
+// lifted by 2^15, which leaves them below 2^16 and keeps the bits of small ones.
+//
+// delta = dout . out comes from an out that was rounded.  Where all of a row's
+// keys are in one tile (the first rows of a causal sequence, whose out is
+// largest) the dq kernel takes it from P and dP instead, for itself and for the
+// kernel of dk and dv, which runs after it.
 #include "na_packed_tc.cuh"
 
 namespace na2d {
@@ -34,44 +40,61 @@ using namespace packed;
 
 template <int D> struct Bwd {
   using G = Geo<D>;
-  static constexpr int STAGES = D == 128 ? 2 : 4;
-  static constexpr int RING_OFF = 2 * G::TILE_BYTES;  // the two tiles that stay come first
-  static constexpr int TERMS_OFF = RING_OFF + STAGES * 2 * G::TILE_BYTES;
-  static constexpr int BAR_OFF = TERMS_OFF + STAGES * 2 * kTile * 4;
-  static constexpr int SMEM = BAR_OFF + 256 + 1024;
+  // slots of the rings: A for Q (K), which are needed first and kept longest, B
+  // for dO (V)
+  static constexpr int SA = D == 128 ? 3 : 4, SB = D == 128 ? 2 : 4, ST = 2;
+  static constexpr int A_OFF = 2 * G::TILE_BYTES;  // the two tiles that stay come first
+  static constexpr int B_OFF = A_OFF + SA * G::TILE_BYTES;
+  static constexpr int TERMS_OFF = B_OFF + SB * G::TILE_BYTES;
+  static constexpr int BAR_OFF = TERMS_OFF + ST * 2 * kTile * 4;
+  static constexpr int SMEM = BAR_OFF + 256;
   static constexpr int SMEM_ASKED = SMEM > 116 * 1024 ? SMEM : 116 * 1024;  // one block an SM: it holds all of tensor memory
   static_assert(SMEM <= kMaxSmem, "fits");
   static constexpr int THREADS = 384;
   static constexpr int REGS_CTRL = 72, REGS_WORK = 216;
+  static constexpr int kBars = 7 + 2 * SA + 2 * SB + 2 * ST;
+  static_assert(kBars * 8 + 8 <= 256, "fits");
 };
 
-struct Bars {
+// The barriers, and the two words behind them: tensor memory's address and the
+// block's abort flag.
+template <int D> struct Bars {
+  using C = Bwd<D>;
   uint32_t base;
-  int stages;
   NA_DEVICE uint32_t kept() const { return base; }
-  NA_DEVICE uint32_t tail() const { return base + 8; }
-  NA_DEVICE uint32_t done() const { return base + 16; }
-  NA_DEVICE uint32_t s() const { return base + 24; }
-  NA_DEVICE uint32_t dp() const { return base + 32; }
-  NA_DEVICE uint32_t p_ready() const { return base + 40; }
-  NA_DEVICE uint32_t ds_ready() const { return base + 48; }
-  NA_DEVICE uint32_t full(int i) const { return base + 56 + (i % stages) * 8; }
-  NA_DEVICE uint32_t empty(int i) const { return base + 56 + (stages + i % stages) * 8; }
-  NA_DEVICE void init(int full_count) const {
+  NA_DEVICE uint32_t done() const { return base + 8; }
+  NA_DEVICE uint32_t s() const { return base + 16; }
+  NA_DEVICE uint32_t dp() const { return base + 24; }
+  NA_DEVICE uint32_t p_ready() const { return base + 32; }
+  NA_DEVICE uint32_t ds_ready() const { return base + 40; }
+  NA_DEVICE uint32_t tail() const { return base + 48; }  // of both rings' last tile
+  NA_DEVICE uint32_t full_a(int i) const { return base + 56 + (i % C::SA) * 8; }
+  NA_DEVICE uint32_t empty_a(int i) const { return base + 56 + (C::SA + i % C::SA) * 8; }
+  NA_DEVICE uint32_t full_b(int i) const { return base + 56 + (2 * C::SA + i % C::SB) * 8; }
+  NA_DEVICE uint32_t empty_b(int i) const { return base + 56 + (2 * C::SA + C::SB + i % C::SB) * 8; }
+  NA_DEVICE uint32_t full_t(int i) const { return base + 56 + (2 * C::SA + 2 * C::SB + i % C::ST) * 8; }
+  NA_DEVICE uint32_t empty_t(int i) const { return base + 56 + (2 * C::SA + 2 * C::SB + C::ST + i % C::ST) * 8; }
+  NA_DEVICE uint32_t tmem_slot() const { return base + 248; }
+  NA_DEVICE void init(int empty_b_count) const {
     mbar_init(kept(), 1);
-    mbar_init(tail(), 1);
     mbar_init(done(), 2);  // both MMA warps'
     mbar_init(s(), 1);
     mbar_init(dp(), 1);
     mbar_init(p_ready(), 8);
     mbar_init(ds_ready(), 8);
-    for (int i = 0; i < stages; ++i) {
-      mbar_init(full(i), full_count);
-      mbar_init(empty(i), 2);
-    }
+    mbar_init(tail(), 2);
+    for (int i = 0; i < C::SA; ++i) mbar_init(full_a(i), 1), mbar_init(empty_a(i), 1);
+    for (int i = 0; i < C::SB; ++i) mbar_init(full_b(i), 1), mbar_init(empty_b(i), empty_b_count);
+    for (int i = 0; i < C::ST; ++i) mbar_init(full_t(i), 1), mbar_init(empty_t(i), 8);
     mbar_init_fence();
   }
 };
+// Shared memory is asked for without room to align it: tiles need 1024 bytes.
+NA_DEVICE bool aligned_or_report(uint32_t base, unsigned* status) {
+  if ((base & 1023u) == 0) return true;
+  if (threadIdx.x == 0) atomicOr(status, kStatusTimeout);
+  return false;
+}
 
 template <int W> NA_DEVICE void tmem_ld_n(uint32_t at, uint32_t (&r)[W]) {
   if constexpr (W == 32)
@@ -123,15 +146,15 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
   using C = Bwd<D>;
   using G = Geo<D>;
   constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value;
-  extern __shared__ uint8_t raw[];
-  __shared__ uint32_t tmem_slot;
-  __shared__ volatile int abort_flag;
+  extern __shared__ __align__(1024) uint8_t raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  const int P = kTile / p.group, kh = blockIdx.y, Z = p.max_pieces;
+  // heads and pieces first, then tiles: the heavy tiles of all heads start first
+  const int P = kTile / p.group, Z = p.max_pieces, lanes_of_tile = p.hk * Z;
+  const int kh = blockIdx.x % lanes_of_tile / Z, z = blockIdx.x % Z;
   int s;
   long long idx;
-  find_part_warp(p.cu_k, p.nseq, p.total_k, 1, kTile, blockIdx.x, &s, &idx);
+  find_part_warp(p.cu_k, p.nseq, p.total_k, 1, kTile, blockIdx.x / lanes_of_tile, &s, &idx);
   if (idx < 0) return;
   const Span sp = span_of(p, s);
   if (idx * kTile >= sp.nk) return;
@@ -140,86 +163,72 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
   int first, last, unused;
   seen_by(p, sp, j0, &first, &unused);
   seen_by(p, sp, j0 + nk - 1, &unused, &last);
-  const int tiles = last > first ? (last - first + P - 1) / P : 0, z = blockIdx.z;
+  const int tiles = last > first ? (last - first + P - 1) / P : 0;
   const int n = tiles > z ? (tiles - z + Z - 1) / Z : 0;
   auto tile_pos = [&](int i) { return first + (z + i * Z) * P; };
 
-  const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
+  const uint32_t base = smem_addr(raw);
+  if (!aligned_or_report(base, p.status)) return;
   const uint32_t k_tile = base, v_tile = base + G::TILE_BYTES;
-  auto q_tile = [&](int i) { return base + C::RING_OFF + (i % C::STAGES) * 2 * G::TILE_BYTES; };
-  auto o_tile = [&](int i) { return q_tile(i) + G::TILE_BYTES; };
-  float* terms = reinterpret_cast<float*>(raw + (base - smem_addr(raw)) + C::TERMS_OFF);
-  auto lse_of = [&](int i) { return terms + (i % C::STAGES) * 2 * kTile; };
-  const Bars bar{base + C::BAR_OFF, C::STAGES};
+  auto q_tile = [&](int i) { return base + C::A_OFF + (i % C::SA) * G::TILE_BYTES; };
+  auto o_tile = [&](int i) { return base + C::B_OFF + (i % C::SB) * G::TILE_BYTES; };
+  auto lse_of = [&](int i) { return reinterpret_cast<float*>(raw + C::TERMS_OFF) + (i % C::ST) * 2 * kTile; };
+  const Bars<D> bar{base + C::BAR_OFF};
+  volatile int* ab = reinterpret_cast<volatile int*>(raw + C::BAR_OFF + 252);
   if (threadIdx.x == 0) {
-    abort_flag = 0;
-    bar.init(2);  // the copies, and the rows' terms
+    *ab = 0;
+    bar.init(2);  // dO goes into dP and dV
   }
-  if (warp == 1) tmem_alloc(smem_addr(&tmem_slot), 512);
+  if (warp == 1) tmem_alloc(bar.tmem_slot(), 512);
   if (P * p.group < kTile && warp >= 4)  // rows of a tile that no copy fills
-    for (int i = warp - 4; i < 2 * C::STAGES; i += 8) zero_rows<D>(base + C::RING_OFF + i * G::TILE_BYTES, P * p.group);
+    for (int i = warp - 4; i < C::SA + C::SB; i += 8) zero_rows<D>(base + C::A_OFF + i * G::TILE_BYTES, P * p.group);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(raw + C::BAR_OFF + 248);
   const uint32_t s_at = tmem, dp_at = tmem + 128, dv_at = tmem + 256, dk_at = tmem + 256 + D;
-  volatile int* ab = &abort_flag;
+  constexpr float kLift = BF16 ? 0.f : 15.f, kUnlift = BF16 ? 1.f : 1.f / 32768.f;
 
   if (warp < 4) {
     regs_dec<C::REGS_CTRL>();
-    if (warp == 0 && n > 0) {
-      // ------------------------------------------------------------- loads
-      if (lane == 0) {
+    if ((warp == 0 || warp == 2) && n > 0) {
+      // ------------------ loads: K, V and the row tiles' Q by one warp, their
+      // log-sum-exp, delta and dO by another
+      const bool first_warp = warp == 0;
+      if (first_warp && lane == 0) {
         mbar_expect_tx(bar.kept(), 2 * G::TILE_BYTES);
         load_key_tile<D>(k_tile, &mk, bar.kept(), kh, sp.k0 + j0);
         load_key_tile<D>(v_tile, &mv, bar.kept(), kh, sp.k0 + j0);
       }
-      const uint32_t bytes = (uint32_t)(2 * P * p.group * D * 2);
-      bool tail_used = false;
+      const uint32_t bytes = (uint32_t)(P * p.group * D * 2);
       int i = 0;
       for (; i < n; ++i) {
-        if (i >= C::STAGES && !mbar_wait(bar.empty(i), ((i / C::STAGES) - 1) & 1, ab, p.status)) break;
         const int pos = tile_pos(i);
-        // rows past the sequence are zeroed: what they hold may be NaN
-        const bool tail = pos + P > sp.nq;
-        const uint32_t b = tail ? bar.tail() : bar.full(i);
-        if (lane == 0) {
-          mbar_expect_tx(b, bytes);
-          load_row_tile<D>(q_tile(i), &mq, b, kh, sp.q0 + pos);
-          load_row_tile<D>(o_tile(i), &mo, b, kh, sp.q0 + pos);
-        }
-        __syncwarp();
-        if (tail) {
-          tail_used = true;
-          if (!mbar_wait(bar.tail(), 0, ab, p.status)) break;
-          zero_rows<D>(q_tile(i), (sp.nq - pos) * p.group);
-          zero_rows<D>(o_tile(i), (sp.nq - pos) * p.group);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar.full(i));
-        }
-      }
-      if (*ab) {  // leave no copy in flight
-        mbar_wait_settle(bar.kept(), 0);
-        if (tail_used) mbar_wait_settle(bar.tail(), 0);
-      }
-    } else if (warp == 2 && n > 0) {
-      // ---------------------------------- the rows' log-sum-exp and delta
-      for (int i = 0; i < n; ++i) {
-        if (i >= C::STAGES && !mbar_wait(bar.empty(i), ((i / C::STAGES) - 1) & 1, ab, p.status)) break;
-        const int pos = tile_pos(i);
-        float* lse = lse_of(i);
+        if (!first_warp) {
+          if (i >= C::ST && !mbar_wait(bar.empty_t(i), ((i / C::ST) - 1) & 1, ab, p.status)) break;
+          float* lse = lse_of(i);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = lane + 32 * e, at = r / p.group;
-          float2 t = make_float2(INFINITY, 0.f);  // a row that is not there: weights 0
-          if (at < P && pos + at < sp.nq)
-            t = p.terms[((long long)sp.q0 + pos + at) * p.hq + kh * p.group + (r - at * p.group)];
-          lse[r] = t.x;
-          lse[kTile + r] = t.y;
+          for (int e = 0; e < 4; ++e) {
+            const int r = lane + 32 * e, at = r / p.group;
+            float2 t = make_float2(INFINITY, 0.f);  // a row that is not there: weights 0
+            if (at < P && pos + at < sp.nq)
+              t = p.terms[((long long)sp.q0 + pos + at) * p.hq + kh * p.group + (r - at * p.group)];
+            lse[r] = t.x - kLift;
+            lse[kTile + r] = t.y * kUnlift;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar.full_t(i));
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar.full(i));
+        const uint32_t empty = first_warp ? bar.empty_a(i) : bar.empty_b(i);
+        const int slots = first_warp ? C::SA : C::SB;
+        if (i >= slots && !mbar_wait(empty, ((i / slots) - 1) & 1, ab, p.status)) break;
+        load_ring_tile<D>(first_warp ? q_tile(i) : o_tile(i), first_warp ? bar.full_a(i) : bar.full_b(i), bar.tail(),
+                          (sp.nq - pos) * p.group, P * p.group, bytes, ab, p.status, [&](uint32_t dst, uint32_t b) {
+                            load_row_tile<D>(dst, first_warp ? &mq : &mo, b, kh, sp.q0 + pos);
+                          });
       }
+      if (*ab && first_warp) mbar_wait_settle(bar.kept(), 0);
+      if (*ab) mbar_wait_settle(first_warp ? bar.full_a(max(i, 1) - 1) : bar.full_b(max(i, 1) - 1), 0);
     } else if ((warp == 1 || warp == 3) && n > 0) {
       // -------------------------------------------------------------- MMAs
       // One warp for S^T and dV, one for dP^T and dK: each runs its two in
@@ -233,24 +242,31 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       // S^T is made of a row tile's Q and dV summed with its dO; dP^T and dK the other way round
       auto with = [&](int i) { return first_warp ? q_tile(i) : o_tile(i); };
       auto sums = [&](int i) { return first_warp ? o_tile(i) : q_tile(i); };
-      bool ok = mbar_wait(bar.kept(), 0, ab, p.status) && mbar_wait(bar.full(0), 0, ab, p.status);
+      auto wait_a = [&](int i) { return mbar_wait(bar.full_a(i), (i / C::SA) & 1, ab, p.status); };
+      auto wait_b = [&](int i) { return mbar_wait(bar.full_b(i), (i / C::SB) & 1, ab, p.status); };
+      bool ok = mbar_wait(bar.kept(), 0, ab, p.status) && (first_warp ? wait_a(0) : wait_b(0));
       if (__all_sync(0xffffffffu, ok)) {
         tc_fence_after();
         if (elect_one()) {
           mma_rows_by_rows<D, BF16>(at, kept, with(0));
           mma_commit(made);
+          if (!first_warp) mma_commit(bar.empty_b(0));
         }
         for (int i = 0; i < n; ++i) {
-          ok = i + 1 >= n || mbar_wait(bar.full(i + 1), ((i + 1) / C::STAGES) & 1, ab, p.status);
-          ok = ok && mbar_wait(ready, i & 1, ab, p.status);
+          ok = (first_warp ? wait_b(i) : wait_a(i)) && mbar_wait(ready, i & 1, ab, p.status);
           if (!__all_sync(0xffffffffu, ok)) break;
           tc_fence_after();
           if (elect_one()) {
             mma_weights_by_tile<D, BF16, 64>(to, at, sums(i), i > 0);  // the halves lie 64 columns apart
-            mma_commit(bar.empty(i));
-            if (i + 1 < n) {
+            mma_commit(first_warp ? bar.empty_b(i) : bar.empty_a(i));
+          }
+          if (i + 1 < n) {
+            if (!__all_sync(0xffffffffu, first_warp ? wait_a(i + 1) : wait_b(i + 1))) break;
+            tc_fence_after();
+            if (elect_one()) {
               mma_rows_by_rows<D, BF16>(at, kept, with(i + 1));
               mma_commit(made);
+              if (!first_warp) mma_commit(bar.empty_b(i + 1));
             }
           }
         }
@@ -273,9 +289,7 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     const float sl2 = p.scale * kLog2e;
     bool ok = true;
     for (int i = 0; i < n; ++i) {
-      // the terms were written before the copies' barrier completed, which the
-      // arrival of S^T follows; waiting for it makes them visible here
-      if (!(ok = mbar_wait(bar.full(i), (i / C::STAGES) & 1, ab, p.status))) break;
+      if (!(ok = mbar_wait(bar.full_t(i), (i / C::ST) & 1, ab, p.status))) break;
       if (!(ok = mbar_wait(bar.s(), i & 1, ab, p.status))) break;
       tc_fence_after();
       const int pos = tile_pos(i);
@@ -330,8 +344,8 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
           const float4 l = delta[8 * c + e / 4];
           float f[4] = {__uint_as_float(y[c][e]), __uint_as_float(y[c][e + 1]), __uint_as_float(y[c][e + 2]),
                         __uint_as_float(y[c][e + 3])};
-          add2(f[0], f[1], f[0], f[1], -l.x, -l.y);
-          add2(f[2], f[3], f[2], f[3], -l.z, -l.w);
+          fma2(f[0], f[1], f[0], f[1], kUnlift, kUnlift, -l.x, -l.y);
+          fma2(f[2], f[3], f[2], f[3], kUnlift, kUnlift, -l.z, -l.w);
 #pragma unroll
           for (int u = 0; u < 4; ++u) f[u] *= __uint_as_float(x[c][e + u]);
           w[e / 2] = pack2<T>(f[0], f[1]);
@@ -342,13 +356,16 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar.ds_ready());
+      if (lane == 0) {
+        mbar_arrive(bar.ds_ready());
+        mbar_arrive(bar.empty_t(i));
+      }
     }
     if (ok && n > 0) ok = mbar_wait(bar.done(), 0, ab, p.status);
     if (ok) {
       tc_fence_after();
       // the first warpgroup writes dv, the second dk
-      const float f0 = half ? p.scale : 1.f;
+      const float f0 = half ? p.scale : 1.f, taken = half ? p.scale : kUnlift;
       const uint32_t from = (half ? dk_at : dv_at) + lanes;
       const long long at = ((long long)(sp.k0 + j0 + key) * p.hk + kh) * D;
       T* to = (T*)(half ? p.dk : p.dv) + at;
@@ -362,7 +379,7 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         float f[W];
 #pragma unroll
         for (int e = 0; e < W; ++e) {
-          f[e] = __uint_as_float(o[e]) * f0;
+          f[e] = __uint_as_float(o[e]) * taken;
           finite = finite && fabsf(f[e]) < INFINITY;
         }
         if (live) {
@@ -454,15 +471,13 @@ packed_dq_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
   using C = Bwd<D>;
   using G = Geo<D>;
   constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value;
-  extern __shared__ uint8_t raw[];
-  __shared__ uint32_t tmem_slot;
-  __shared__ volatile int abort_flag;
+  extern __shared__ __align__(1024) uint8_t raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  const int P = kTile / p.group, kh = blockIdx.y;
+  const int P = kTile / p.group, kh = blockIdx.x % p.hk;
   int s;
   long long idx;
-  find_part_warp(p.cu_q, p.nseq, p.total_q, 1, P, blockIdx.x, &s, &idx);
+  find_part_warp(p.cu_q, p.nseq, p.total_q, 1, P, blockIdx.x / p.hk, &s, &idx);
   const Span sp = span_of(p, s);
   const long long part = (sp.nq + P - 1) / P - 1 - idx;  // the rows that see most keys first
   if (idx < 0 || part < 0) return;
@@ -472,63 +487,52 @@ packed_dq_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
   visible(p, sp, min(pos0 + P, sp.nq) - 1, &unused, &ke);
   const int n = ke > kb ? (ke - kb + kTile - 1) / kTile : 0;
 
-  const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
+  const uint32_t base = smem_addr(raw);
+  if (!aligned_or_report(base, p.status)) return;
   const uint32_t q_tile = base, o_tile = base + G::TILE_BYTES;
-  auto k_tile = [&](int i) { return base + C::RING_OFF + (i % C::STAGES) * 2 * G::TILE_BYTES; };
-  auto v_tile = [&](int i) { return k_tile(i) + G::TILE_BYTES; };
-  const Bars bar{base + C::BAR_OFF, C::STAGES};
+  auto k_tile = [&](int i) { return base + C::A_OFF + (i % C::SA) * G::TILE_BYTES; };
+  auto v_tile = [&](int i) { return base + C::B_OFF + (i % C::SB) * G::TILE_BYTES; };
+  const Bars<D> bar{base + C::BAR_OFF};
+  volatile int* ab = reinterpret_cast<volatile int*>(raw + C::BAR_OFF + 252);
   if (threadIdx.x == 0) {
-    abort_flag = 0;
+    *ab = 0;
     bar.init(1);
   }
-  if (warp == 1) tmem_alloc(smem_addr(&tmem_slot), 512);
+  if (warp == 1) tmem_alloc(bar.tmem_slot(), 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(raw + C::BAR_OFF + 248);
   const uint32_t dp_at = tmem + 256, dq_at = tmem + 384;  // S in two slots of 128 columns
-  volatile int* ab = &abort_flag;
 
   if (warp < 4) {
     regs_dec<C::REGS_CTRL>();
-    if (warp == 0 && n > 0) {
-      // ------------------------------------------------------------- loads
-      if (lane == 0) {
+    if ((warp == 0 || warp == 3) && n > 0) {
+      // ------------- loads: Q, dO and the keys by one warp, values by another
+      const bool first_warp = warp == 0;
+      if (first_warp && lane == 0) {
         mbar_expect_tx(bar.kept(), (uint32_t)(2 * P * p.group * D * 2));
         load_row_tile<D>(q_tile, &mq, bar.kept(), kh, sp.q0 + pos0);
         load_row_tile<D>(o_tile, &mo, bar.kept(), kh, sp.q0 + pos0);
       }
-      bool tail_used = false;
       int i = 0;
       for (; i < n; ++i) {
-        if (i >= C::STAGES && !mbar_wait(bar.empty(i), ((i / C::STAGES) - 1) & 1, ab, p.status)) break;
-        const int k0 = kb + i * kTile;
-        const bool tail = k0 + kTile > sp.nk;  // keys past the sequence are zeroed
-        const uint32_t b = tail ? bar.tail() : bar.full(i);
-        if (lane == 0) {
-          mbar_expect_tx(b, 2 * G::TILE_BYTES);
-          load_key_tile<D>(k_tile(i), &mk, b, kh, sp.k0 + k0);
-          load_key_tile<D>(v_tile(i), &mv, b, kh, sp.k0 + k0);
-        }
-        __syncwarp();
-        if (tail) {
-          tail_used = true;
-          if (!mbar_wait(bar.tail(), 0, ab, p.status)) break;
-          zero_rows<D>(k_tile(i), sp.nk - k0);
-          zero_rows<D>(v_tile(i), sp.nk - k0);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar.full(i));
-        }
+        const int k0 = kb + i * kTile, slots = first_warp ? C::SA : C::SB;
+        const uint32_t empty = first_warp ? bar.empty_a(i) : bar.empty_b(i);
+        if (i >= slots && !mbar_wait(empty, ((i / slots) - 1) & 1, ab, p.status)) break;
+        load_ring_tile<D>(first_warp ? k_tile(i) : v_tile(i), first_warp ? bar.full_a(i) : bar.full_b(i), bar.tail(),
+                          sp.nk - k0, kTile, G::TILE_BYTES, ab, p.status, [&](uint32_t dst, uint32_t b) {
+                            load_key_tile<D>(dst, first_warp ? &mk : &mv, b, kh, sp.k0 + k0);
+                          });
       }
-      if (*ab) {  // leave no copy in flight
-        mbar_wait_settle(bar.kept(), 0);
-        if (tail_used) mbar_wait_settle(bar.tail(), 0);
-        for (int u = max(0, i - C::STAGES); u < i; ++u) mbar_wait_settle(bar.full(u), (u / C::STAGES) & 1);
-      }
+      if (*ab && first_warp) mbar_wait_settle(bar.kept(), 0);
+      if (*ab) mbar_wait_settle(first_warp ? bar.full_a(max(i, 1) - 1) : bar.full_b(max(i, 1) - 1), 0);
     } else if ((warp == 1 || warp == 2) && n > 0) {
       // -------------------------------------------------------------- MMAs
       // One warp for S and dQ, one for dP, for the same reason as above.
-      bool ok = mbar_wait(bar.kept(), 0, ab, p.status) && mbar_wait(bar.full(0), 0, ab, p.status);
+      auto wait_a = [&](int i) { return mbar_wait(bar.full_a(i), (i / C::SA) & 1, ab, p.status); };
+      auto wait_b = [&](int i) { return mbar_wait(bar.full_b(i), (i / C::SB) & 1, ab, p.status); };
+      bool ok = mbar_wait(bar.kept(), 0, ab, p.status) && (warp == 1 ? wait_a(0) : wait_b(0));
       if (__all_sync(0xffffffffu, ok)) {
         tc_fence_after();
         if (elect_one()) {
@@ -538,29 +542,30 @@ packed_dq_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
           } else {
             mma_rows_by_rows<D, BF16>(dp_at, o_tile, v_tile(0));
             mma_commit(bar.dp());
-            mma_commit(bar.empty(0));
+            mma_commit(bar.empty_b(0));
           }
         }
         for (int i = 0; i < n; ++i) {
-          if (i + 1 < n) {
-            ok = mbar_wait(bar.full(i + 1), ((i + 1) / C::STAGES) & 1, ab, p.status);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            if (warp == 1 && elect_one()) {
+          if (warp == 1 && i + 1 < n) {
+            if (!__all_sync(0xffffffffu, wait_a(i + 1))) break;
+            tc_fence_after();
+            if (elect_one()) {
               mma_rows_by_rows<D, BF16>(tmem + ((i + 1) & 1) * kTile, q_tile, k_tile(i + 1));
               mma_commit(bar.s());
             }
           }
           ok = mbar_wait(bar.ds_ready(), i & 1, ab, p.status);
+          if (warp == 2 && i + 1 < n) ok = ok && wait_b(i + 1);
           if (!__all_sync(0xffffffffu, ok)) break;
           tc_fence_after();
           if (elect_one()) {
             if (warp == 1) {
               mma_weights_by_tile<D, BF16, 64>(dq_at, tmem + (i & 1) * kTile, k_tile(i), i > 0);
-              mma_commit(bar.empty(i));
+              mma_commit(bar.empty_a(i));
             } else if (i + 1 < n) {
               mma_rows_by_rows<D, BF16>(dp_at, o_tile, v_tile(i + 1));
               mma_commit(bar.dp());
-              mma_commit(bar.empty(i + 1));
+              mma_commit(bar.empty_b(i + 1));
             }
           }
         }
@@ -580,12 +585,17 @@ packed_dq_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
     int lo, hi;
     visible(p, sp, live ? pos : pos0, &lo, &hi);
     const int all_lo = __reduce_max_sync(0xffffffffu, lo), all_hi = __reduce_min_sync(0xffffffffu, hi);
-    const float2 term = p.terms[out_row];
+    float2 term = p.terms[out_row];
     const float sl2 = p.scale * kLog2e;
     bool ok = true;
+    // both warpgroups meet once where n is 1, also when one has given up
+    auto meet = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
     for (int i = 0; i < n; ++i) {
       const uint32_t my_s = tmem + lanes + (i & 1) * kTile + half * 64, my_dp = dp_at + lanes + half * 64;
-      if (!(ok = mbar_wait(bar.s(), i & 1, ab, p.status))) break;
+      if (!(ok = mbar_wait(bar.s(), i & 1, ab, p.status))) {
+        if (n == 1) meet();
+        break;
+      }
       tc_fence_after();
       const int k0 = kb + i * kTile;
       const bool masked = k0 < all_lo || k0 + kTile > all_hi;
@@ -605,7 +615,10 @@ packed_dq_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
           x[c][e] = __float_as_uint(ex2(f0));
           x[c][e + 1] = __float_as_uint(ex2(f1));
         }
-      if (!(ok = mbar_wait(bar.dp(), i & 1, ab, p.status))) break;
+      if (!(ok = mbar_wait(bar.dp(), i & 1, ab, p.status))) {
+        if (n == 1) meet();
+        break;
+      }
       tc_fence_after();
       uint32_t y[2][32];
       tmem_ld32(my_dp, y[0]);
@@ -613,6 +626,21 @@ packed_dq_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
       tmem_wait_ld_regs(y[0]);
       tmem_wait_ld_regs(y[1]);
       if (masked) mask_outside(y, a, b, 0u);
+      if (n == 1) {
+        // all of the row's weights are here: delta from them
+        float d0 = 0.f, d1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; e += 2)
+            fma2(d0, d1, __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]), __uint_as_float(y[c][e]),
+                 __uint_as_float(y[c][e + 1]), d0, d1);
+        float* sums = reinterpret_cast<float*>(raw + C::TERMS_OFF);
+        sums[half * kTile + row] = d0 + d1;
+        meet();
+        term.y = sums[row] + sums[kTile + row];
+        if (live && half == 0) p.terms[out_row].y = term.y;
+      }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         uint32_t w[16];
@@ -691,7 +719,7 @@ template <typename T, int D> cudaError_t launch(const PackedArgs& p, cudaStream_
   constexpr int kRegs = 128 * C::REGS_CTRL + 256 * C::REGS_WORK;
   const long long kb = part_numbers(p.nseq, p.total_k, 1, kTile);
   const long long qb = part_numbers(p.nseq, p.total_q, 1, kTile / p.group);
-  if (kb > 0x7fffffffLL || qb > 0x7fffffffLL) return cudaErrorInvalidValue;
+  if (kb * p.hk * p.max_pieces > 0x7fffffffLL || qb * p.hk > 0x7fffffffLL) return cudaErrorInvalidValue;
   cudaError_t e = prepare_kernel<packed_dkdv_tc_kernel<T, D>>(C::SMEM_ASKED, C::THREADS, kRegs);
   if (e == cudaSuccess) e = prepare_kernel<packed_dq_tc_kernel<T, D>>(C::SMEM_ASKED, C::THREADS, kRegs);
   if (e != cudaSuccess) return e;
@@ -699,16 +727,17 @@ template <typename T, int D> cudaError_t launch(const PackedArgs& p, cudaStream_
   if (!row_map(&mq, p.q, p, bf16) || !row_map(&mo, p.dout, p, bf16) || !key_map(&mk, p.k, p, bf16) ||
       !key_map(&mv, p.v, p, bf16))
     return cudaErrorInvalidValue;
-  packed_dkdv_tc_kernel<T, D><<<dim3((unsigned)kb, (unsigned)p.hk, (unsigned)p.max_pieces), C::THREADS,
-                                C::SMEM_ASKED, st>>>(mq, mo, mk, mv, p);
+  // dq first: it improves rows' delta on its way
+  packed_dq_tc_kernel<T, D><<<(unsigned)(qb * p.hk), C::THREADS, C::SMEM_ASKED, st>>>(mq, mo, mk, mv, p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  packed_dkdv_tc_kernel<T, D>
+      <<<(unsigned)(kb * p.hk * p.max_pieces), C::THREADS, C::SMEM_ASKED, st>>>(mq, mo, mk, mv, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (p.max_pieces > 1) {
     const long long blocks = ((long long)p.total_k * p.hk * (D / 8) + 255) / 256;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
     packed_dkdv_join_kernel<T><<<dim3((unsigned)blocks, 2), 256, 0, st>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  packed_dq_tc_kernel<T, D><<<dim3((unsigned)qb, (unsigned)p.hk), C::THREADS, C::SMEM_ASKED, st>>>(mq, mo, mk, mv, p);
   return cudaGetLastError();
 }
 template <typename T> cudaError_t launch_d(const PackedArgs& p, cudaStream_t st) {
