@@ -52,7 +52,7 @@ template <int D> struct Bwd {
   static_assert(SMEM <= kMaxSmem, "fits");
   static constexpr int THREADS = 384;
   static constexpr int REGS_CTRL = 72, REGS_WORK = 216;
-  static constexpr int kBars = 7 + 2 * SA + 2 * SB + 2 * ST;
+  static constexpr int kBars = 9 + 2 * SA + 2 * SB + 2 * ST;
   static_assert(kBars * 8 + 8 <= 256, "fits");
 };
 
@@ -68,12 +68,14 @@ template <int D> struct Bars {
   NA_DEVICE uint32_t p_ready() const { return base + 32; }
   NA_DEVICE uint32_t ds_ready() const { return base + 40; }
   NA_DEVICE uint32_t tail() const { return base + 48; }  // of both rings' last tile
-  NA_DEVICE uint32_t full_a(int i) const { return base + 56 + (i % C::SA) * 8; }
-  NA_DEVICE uint32_t empty_a(int i) const { return base + 56 + (C::SA + i % C::SA) * 8; }
-  NA_DEVICE uint32_t full_b(int i) const { return base + 56 + (2 * C::SA + i % C::SB) * 8; }
-  NA_DEVICE uint32_t empty_b(int i) const { return base + 56 + (2 * C::SA + C::SB + i % C::SB) * 8; }
-  NA_DEVICE uint32_t full_t(int i) const { return base + 56 + (2 * C::SA + 2 * C::SB + i % C::ST) * 8; }
-  NA_DEVICE uint32_t empty_t(int i) const { return base + 56 + (2 * C::SA + 2 * C::SB + C::ST + i % C::ST) * 8; }
+  NA_DEVICE uint32_t p_half() const { return base + 64; }
+  NA_DEVICE uint32_t turn() const { return base + 56; }  // of the other MMA warp
+  NA_DEVICE uint32_t full_a(int i) const { return base + 72 + (i % C::SA) * 8; }
+  NA_DEVICE uint32_t empty_a(int i) const { return base + 72 + (C::SA + i % C::SA) * 8; }
+  NA_DEVICE uint32_t full_b(int i) const { return base + 72 + (2 * C::SA + i % C::SB) * 8; }
+  NA_DEVICE uint32_t empty_b(int i) const { return base + 72 + (2 * C::SA + C::SB + i % C::SB) * 8; }
+  NA_DEVICE uint32_t full_t(int i) const { return base + 72 + (2 * C::SA + 2 * C::SB + i % C::ST) * 8; }
+  NA_DEVICE uint32_t empty_t(int i) const { return base + 72 + (2 * C::SA + 2 * C::SB + C::ST + i % C::ST) * 8; }
   NA_DEVICE uint32_t tmem_slot() const { return base + 248; }
   NA_DEVICE void init(int empty_b_count) const {
     mbar_init(kept(), 1);
@@ -81,8 +83,10 @@ template <int D> struct Bars {
     mbar_init(s(), 1);
     mbar_init(dp(), 1);
     mbar_init(p_ready(), 8);
+    mbar_init(p_half(), 8);
     mbar_init(ds_ready(), 8);
     mbar_init(tail(), 2);
+    mbar_init(turn(), 1);
     for (int i = 0; i < C::SA; ++i) mbar_init(full_a(i), 1), mbar_init(empty_a(i), 1);
     for (int i = 0; i < C::SB; ++i) mbar_init(full_b(i), 1), mbar_init(empty_b(i), empty_b_count);
     for (int i = 0; i < C::ST; ++i) mbar_init(full_t(i), 1), mbar_init(empty_t(i), 8);
@@ -233,7 +237,8 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       // -------------------------------------------------------------- MMAs
       // One warp for S^T and dV, one for dP^T and dK: each runs its two in
       // turn, and while one looks at its barriers the tensor pipe has the
-      // other's.  The whole warp walks the steps, which keeps what the operands
+      // other's.  dK waits until the next S^T is issued, which the threads need
+      // first: all at once, S^T came 0.9 thousand cycles of a step later.  The whole warp walks the steps, which keeps what the operands
       // are made of in uniform registers, and one lane issues.
       const bool first_warp = warp == 1;
       const uint32_t at = first_warp ? s_at : dp_at, to = first_warp ? dv_at : dk_at;
@@ -253,21 +258,38 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
           if (!first_warp) mma_commit(bar.empty_b(0));
         }
         for (int i = 0; i < n; ++i) {
-          ok = (first_warp ? wait_b(i) : wait_a(i)) && mbar_wait(ready, i & 1, ab, p.status);
+          // the next tile is there long before it is needed; asking for it here
+          // keeps the question out of the way between two products
+          ok = first_warp ? wait_b(i) : wait_a(i);
+          if (i + 1 < n) ok = ok && (first_warp ? wait_a(i + 1) : wait_b(i + 1));
+          if (first_warp) {
+            // P^T comes in halves: 32 of each warpgroup's 64 columns
+            ok = ok && mbar_wait(bar.p_half(), i & 1, ab, p.status);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            if (elect_one()) {
+              mma_weights_by_tile<D, BF16, 64, 0, 2>(to, at, sums(i), i > 0);  // the halves lie 64 columns apart
+              mma_weights_by_tile<D, BF16, 64, 4, 6>(to, at, sums(i), true);
+            }
+          }
+          ok = ok && mbar_wait(ready, i & 1, ab, p.status);
+          if (!first_warp) ok = ok && mbar_wait(bar.turn(), i & 1, ab, p.status);
           if (!__all_sync(0xffffffffu, ok)) break;
           tc_fence_after();
           if (elect_one()) {
-            mma_weights_by_tile<D, BF16, 64>(to, at, sums(i), i > 0);  // the halves lie 64 columns apart
+            if (first_warp) {
+              mma_weights_by_tile<D, BF16, 64, 2, 4>(to, at, sums(i), true);
+              mma_weights_by_tile<D, BF16, 64, 6, 8>(to, at, sums(i), true);
+            } else {
+              mma_weights_by_tile<D, BF16, 64>(to, at, sums(i), i > 0);
+            }
             mma_commit(first_warp ? bar.empty_b(i) : bar.empty_a(i));
-          }
-          if (i + 1 < n) {
-            if (!__all_sync(0xffffffffu, first_warp ? wait_a(i + 1) : wait_b(i + 1))) break;
-            tc_fence_after();
-            if (elect_one()) {
+            if (i + 1 < n) {
               mma_rows_by_rows<D, BF16>(at, kept, with(i + 1));
               mma_commit(made);
               if (!first_warp) mma_commit(bar.empty_b(i + 1));
             }
+            if (first_warp) mbar_arrive(bar.turn());
           }
         }
       }
@@ -322,11 +344,11 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
           w[e / 2 + 1] = pack2<T>(f[2], f[3]);
         }
         tmem_st16(my_s + 16 * c, w);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(c == 0 ? bar.p_half() : bar.p_ready());
       }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar.p_ready());
       if (!(ok = mbar_wait(bar.dp(), i & 1, ab, p.status))) break;
       tc_fence_after();
       uint32_t y[2][32];
@@ -529,7 +551,8 @@ packed_dq_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
       if (*ab) mbar_wait_settle(first_warp ? bar.full_a(max(i, 1) - 1) : bar.full_b(max(i, 1) - 1), 0);
     } else if ((warp == 1 || warp == 2) && n > 0) {
       // -------------------------------------------------------------- MMAs
-      // One warp for S and dQ, one for dP, for the same reason as above.
+      // One warp for S and dQ, one for dP, for the same reason as above; dQ waits
+      // until the next dP is issued.
       auto wait_a = [&](int i) { return mbar_wait(bar.full_a(i), (i / C::SA) & 1, ab, p.status); };
       auto wait_b = [&](int i) { return mbar_wait(bar.full_b(i), (i / C::SB) & 1, ab, p.status); };
       bool ok = mbar_wait(bar.kept(), 0, ab, p.status) && (warp == 1 ? wait_a(0) : wait_b(0));
@@ -555,6 +578,7 @@ packed_dq_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
             }
           }
           ok = mbar_wait(bar.ds_ready(), i & 1, ab, p.status);
+          if (warp == 1) ok = ok && mbar_wait(bar.turn(), i & 1, ab, p.status);
           if (warp == 2 && i + 1 < n) ok = ok && wait_b(i + 1);
           if (!__all_sync(0xffffffffu, ok)) break;
           tc_fence_after();
@@ -562,10 +586,13 @@ packed_dq_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
             if (warp == 1) {
               mma_weights_by_tile<D, BF16, 64>(dq_at, tmem + (i & 1) * kTile, k_tile(i), i > 0);
               mma_commit(bar.empty_a(i));
-            } else if (i + 1 < n) {
-              mma_rows_by_rows<D, BF16>(dp_at, o_tile, v_tile(i + 1));
-              mma_commit(bar.dp());
-              mma_commit(bar.empty_b(i + 1));
+            } else {
+              if (i + 1 < n) {
+                mma_rows_by_rows<D, BF16>(dp_at, o_tile, v_tile(i + 1));
+                mma_commit(bar.dp());
+                mma_commit(bar.empty_b(i + 1));
+              }
+              mbar_arrive(bar.turn());
             }
           }
         }
