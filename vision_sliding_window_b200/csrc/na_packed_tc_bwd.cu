@@ -325,6 +325,8 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       tmem_wait_ld_regs(x[0]);
       tmem_wait_ld_regs(x[1]);
       if (masked) mask_outside(x, a, b, 0xff800000u);
+      // a quarter by polynomial, but not where masked places must give exactly 0
+      auto weights = [&](auto poly) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         uint32_t w[16];
@@ -335,11 +337,16 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
                         __uint_as_float(x[c][e + 3])};
           fma2(f[0], f[1], f[0], f[1], sl2, sl2, -l.x, -l.y);
           fma2(f[2], f[3], f[2], f[3], sl2, sl2, -l.z, -l.w);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            f[u] = ex2(f[u]);
-            x[c][e + u] = __float_as_uint(f[u]);
+          f[0] = ex2(f[0]);
+          f[1] = ex2(f[1]);
+          if (decltype(poly)::value && e % 8 == 4) {
+            exp2_poly2(f[2], f[3]);
+          } else {
+            f[2] = ex2(f[2]);
+            f[3] = ex2(f[3]);
           }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) x[c][e + u] = __float_as_uint(f[u]);
           w[e / 2] = pack2<T>(f[0], f[1]);
           w[e / 2 + 1] = pack2<T>(f[2], f[3]);
         }
@@ -349,6 +356,11 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         __syncwarp();
         if (lane == 0) mbar_arrive(c == 0 ? bar.p_half() : bar.p_ready());
       }
+      };
+      if (masked)
+        weights(std::false_type{});
+      else
+        weights(std::true_type{});
       if (!(ok = mbar_wait(bar.dp(), i & 1, ab, p.status))) break;
       tc_fence_after();
       uint32_t y[2][32];
@@ -633,15 +645,27 @@ packed_dq_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
       tmem_wait_ld_regs(x[0]);
       tmem_wait_ld_regs(x[1]);
       if (masked) mask_outside(x, a, b, 0xff800000u);
+      auto weights = [&](auto poly) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          float f0 = __uint_as_float(x[c][e]), f1 = __uint_as_float(x[c][e + 1]);
-          fma2(f0, f1, f0, f1, sl2, sl2, -term.x, -term.x);
-          x[c][e] = __float_as_uint(ex2(f0));
-          x[c][e + 1] = __float_as_uint(ex2(f1));
-        }
+          for (int e = 0; e < 32; e += 2) {
+            float f0 = __uint_as_float(x[c][e]), f1 = __uint_as_float(x[c][e + 1]);
+            fma2(f0, f1, f0, f1, sl2, sl2, -term.x, -term.x);
+            if (decltype(poly)::value && e % 8 == 6) {
+              exp2_poly2(f0, f1);
+            } else {
+              f0 = ex2(f0);
+              f1 = ex2(f1);
+            }
+            x[c][e] = __float_as_uint(f0);
+            x[c][e + 1] = __float_as_uint(f1);
+          }
+      };
+      if (masked)
+        weights(std::false_type{});
+      else
+        weights(std::true_type{});
       if (!(ok = mbar_wait(bar.dp(), i & 1, ab, p.status))) {
         if (n == 1) meet();
         break;
