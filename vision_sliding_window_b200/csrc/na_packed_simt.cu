@@ -587,15 +587,19 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 // type alone.
 //
 // Few rows a sequence (16 on average: single tokens of up to 16 heads a group)
-// run a block for each piece of keys; float32, groups wider than a row tile
-// and calls without keys run on the CUDA cores; the rest on the tensor cores.
+// run the kernel for few rows; float32, groups wider than a row tile and calls
+// without keys run on the CUDA cores; the rest on the tensor cores.
 //
-// A cut of the keys pays where the row tiles alone leave SMs idle.  Kernels
-// that own a few rows cut every sequence into pieces of one length, as long as
-// leaves about `want` blocks but not under 256 keys (each piece's rows pay for
-// writing and joining a float32 output), so that long sequences make more
-// pieces than short ones.  The tensor-core kernel cuts every sequence into the
-// same number of pieces of 512 keys at least, as its grid counts row tiles.
+// A cut of the keys pays where the rows alone leave SMs idle.  The kernel for
+// few rows shares a sequence's keys among 8 blocks by itself and cuts only
+// where sequences times heads are fewer than 19, which leaves SMs without a
+// block, and sequences are longer than 4096 keys on average, of which a block's
+// share takes longer than a second launch.  It and the CUDA-core kernel cut every sequence into pieces of one
+// length, as long as leaves about `want` blocks but not under 256 keys (each
+// piece's rows pay for writing and joining a float32 output), so that long
+// sequences make more pieces than short ones.  The tensor-core kernel cuts
+// every sequence into the same number of pieces of 512 keys at least, as its
+// grid counts row tiles.
 void packed_plan(PackedArgs* p, na_dtype dt) {
   constexpr long long kSms = 148, kMost = 256ll << 20;
   p->piece_keys = 0;
@@ -612,15 +616,16 @@ void packed_plan(PackedArgs* p, na_dtype dt) {
     if (pieces > 1) p->max_pieces = (int)pieces;
     return;
   }
+  if (p->path == kPathRows && ((long long)p->nseq * p->hk * 8 >= kSms || p->total_k / p->nseq <= 4096)) return;
   const int rows = few ? 16 : 64;
-  const long long want = (p->path == kPathRows ? 16 : 8) * kSms, least = 256;
+  const long long want = (p->path == kPathRows ? 4 : 8) * kSms, least = 256;
   const long long per_seq = ((long long)p->total_q * p->group / p->nseq + rows) / rows;  // row tiles, about
   if (per_seq * p->nseq * p->hk >= 4 * kSms) return;
   long long keys = (long long)p->total_k * p->hk * per_seq / want;
   if (keys < least) keys = least;
   keys = (keys + 127) / 128 * 128;
   while (keys < p->total_k && (p->total_k + keys - 1) / keys * row_bytes > kMost) keys *= 2;
-  if (p->total_k == 0 || keys >= p->total_k / p->nseq) return;
+  if (p->total_k == 0 || keys >= p->total_k / p->nseq) return;  // a sequence of average length makes one
   p->piece_keys = (int)keys;
   p->max_pieces = (int)((p->total_k + keys - 1) / keys);
 }

@@ -175,13 +175,13 @@ inline CUtensorMapSwizzle swizzle_of(int row_bytes) {
   return row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
                           : row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
 }
-// [total_k][hk][d] with a box of 128 keys of one head.
-inline bool key_map(CUtensorMap* m, const void* base, const PackedArgs& p, bool bf16) {
+// [total_k][hk][d] with a box of `keys` keys of one head.
+inline bool key_map(CUtensorMap* m, const void* base, const PackedArgs& p, bool bf16, int keys = kTile) {
   auto enc = encode_fn();
   if (!enc) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)p.d, (cuuint64_t)p.hk, (cuuint64_t)p.total_k};
   const cuuint64_t strides[2] = {(cuuint64_t)p.d * 2, (cuuint64_t)p.hk * p.d * 2};
-  const cuuint32_t box[3] = {(cuuint32_t)(p.d > 64 ? 64 : p.d), 1, kTile};
+  const cuuint32_t box[3] = {(cuuint32_t)(p.d > 64 ? 64 : p.d), 1, (cuuint32_t)keys};
   const cuuint32_t one[3] = {1, 1, 1};
   return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
              const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
