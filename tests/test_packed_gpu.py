@@ -72,6 +72,8 @@ FORWARD = [
     ([2100], [2100], 2, 1, 128, "bf16", True, 0),
     ([1500, 600], [1500, 600], 4, 4, 128, "f16", False, 0),
     ([31, 900], [31, 900], 130, 1, 16, "bf16", True, 0),        # more heads in a group than a tile has rows
+    ([100, 20], [3000, 40], 2, 1, 64, "f32", True, 0),          # keys cut into pieces
+    ([70], [2500], 4, 2, 128, "f32", False, 0),
 ]
 
 
@@ -180,6 +182,9 @@ BACKWARD = [
     ([90, 300], [90, 300], 2, 2, 16, "f32", True, 50),
     ([1100], [1100], 2, 1, 128, "f16", True, 0),
     ([31, 200], [31, 200], 130, 1, 16, "bf16", True, 0),
+    ([600, 40], [600, 40], 4, 1, 64, "f32", True, 0),           # walks over rows cut into pieces
+    ([400, 33], [700, 50], 4, 2, 128, "f32", True, 100),
+    ([300], [200], 8, 1, 32, "f32", False, 0),
 ]
 
 

@@ -103,6 +103,7 @@ cudaError_t launch_packed_forward_rows(const PackedArgs& p, na_dtype dt, cudaStr
 cudaError_t launch_packed_forward_tc(const PackedArgs& p, na_dtype dt, cudaStream_t st);    // na_packed_tc.cu
 void packed_backward_plan(PackedArgs* p, na_dtype dt);  // sets path and max_pieces
 cudaError_t launch_packed_backward_tc(const PackedArgs& p, na_dtype dt, cudaStream_t st);   // na_packed_tc_bwd.cu
+cudaError_t launch_packed_dkdv_join(const PackedArgs& p, na_dtype dt, cudaStream_t st);     // there too: adds pieces
 size_t packed_workspace_bytes(const PackedArgs& p, na_dtype dt);
 size_t packed_backward_workspace_bytes(const PackedArgs& p, na_dtype dt);
 cudaError_t launch_packed_forward(PackedArgs p, void* workspace, na_dtype dt, cudaStream_t st);

@@ -125,13 +125,12 @@ template <> NA_DEVICE __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __fl
 
 // two values rounded and packed, a in the low half
 template <typename T> NA_DEVICE uint32_t pack2(float a, float b) {
+  static_assert(sizeof(T) == 2);
   uint32_t r;
-  if constexpr (sizeof(T) == 2) {
-    if constexpr (__is_same(T, __half))
-      asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-    else
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-  }
+  if constexpr (__is_same(T, __half))
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  else
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
   return r;
 }
 

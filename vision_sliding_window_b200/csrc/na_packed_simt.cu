@@ -2,23 +2,32 @@
 // gradients, and the join of partial results; for float32, and for the shapes
 // that the tensor-core kernels do not take.
 //
-// Forward.  A block owns kRows rows (one key head's) and walks the keys they
-// see in tiles of 64 with a running maximum and sum; S and the output stay in
-// registers, each thread a 4 x 8 patch of S and 4 rows x d/8 columns of the
-// output, fed from float32 tiles in shared memory by 16-byte loads: 128 FMAs
-// for 12 loads in S, so FMA issue bounds it, not shared memory.  With few
-// rows (single tokens) 16-row tiles waste less of a tile.
+// Forward.  A block owns 32 rows (16 with single tokens) of one key head and
+// walks the keys they see in tiles of 64 with a running maximum and sum.  S and
+// the output stay in registers, each thread a 2 x 8 patch of S and 2 rows x d/8
+// columns of the output, fed from float32 tiles in shared memory by 16-byte
+// loads.  float32 tiles are copied asynchronously: the next keys come while the
+// softmax and the second product run, the next values while S is made.  Shared
+// memory's 128 bytes a clock bound it: 10 loads of 4 clocks for 64 FMAs.  Rows
+// of 32 rather than 64, in 128 threads, leave more blocks to an SM: 700 + 33 +
+// 512 + 257 rows of 8 heads, d = 64, window 200, take 39 us, against 54 in
+// blocks of 64 rows and 256 threads; only a batch without a mask that fills
+// the device by far (3000 rows of 16 heads) gains 3% from the latter.
 //
 // Backward.  P and dS are recomputed from the rows' log-sum-exp, once with a
 // block owning 64 keys (dk, dv) and once with a block owning 64 rows (dq): two
 // more products than one kernel that adds dq with atomics, but each gradient
-// is one block's sum in a fixed order.
+// is one block's sum in a fixed order.  256 threads a block, as its shared
+// memory leaves room for two an SM where d <= 64 and one where d = 128; the
+// walk over a key tile's rows is cut where key tiles are few (3453 rows, 8 heads
+// on 2, d = 64: 490 us, 870 uncut in 128 threads).
 //
 // A product never touches a masked entry: weights of masked places are
 // skipped, not multiplied by zero, so that what they hold (NaN, infinities)
 // cannot reach a result.
 #include <type_traits>
 
+#include "na2d_sm100.cuh"
 #include "na_packed.cuh"
 
 namespace na2d {
@@ -27,25 +36,31 @@ namespace {
 using namespace packed;
 
 constexpr int kKeys = 64;  // keys of a tile
-constexpr int kThreads = 128;
+constexpr int kLdW = kKeys + 4;  // floats a row of staged weights: read by 16-byte loads
 
-// Loads `n` vectors' worth of a row of D elements into shared float32.
-template <typename T, int D> NA_DEVICE void load_vec(const T* g, float* s, int v, bool live) {
-  constexpr int VEC = 16 / sizeof(T);
-  float f[VEC];
-  if (live) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(g) + v);
+// Brings 16 bytes of a row, as float32, into shared memory; zeros where not
+// live.  float32 goes by itself (wait_copies), other types through registers.
+template <typename T> NA_DEVICE void load_vec(const T* g, float* s, int v, bool live) {
+  if constexpr (sizeof(T) == 4) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sm100::smem_addr(s + v * 4)), "l"(g + v * 4),
+                 "r"(live ? 16 : 0)
+                 : "memory");
+  } else {
+    constexpr int VEC = 16 / sizeof(T);
+    float f[VEC];
+    const uint4 u = live ? __ldg(reinterpret_cast<const uint4*>(g) + v) : make_uint4(0, 0, 0, 0);
     const T* e = reinterpret_cast<const T*>(&u);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) f[i] = to_f<T>(e[i]);
-  } else {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) f[i] = 0.f;
+    for (int i = 0; i < VEC; i += 4)
+      *reinterpret_cast<float4*>(s + v * VEC + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
   }
-#pragma unroll
-  for (int i = 0; i < VEC; i += 4)
-    *reinterpret_cast<float4*>(s + v * VEC + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
 }
+// A thread's copies since the last call are a group; wait_copies<N> leaves the
+// N newest groups in flight.
+NA_DEVICE void end_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> NA_DEVICE void wait_copies() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 template <int D> struct Tile {
   static constexpr int LD = D + 4;  // floats a staged row: 16-byte loads of 8 rows fall on distinct banks
@@ -55,38 +70,41 @@ template <int D> struct Tile {
 
 // Rows [r0, r0 + n) of one key head's rows of a sequence (position r / G, head
 // r % G) from a tensor [total_q][hq][D].
-template <typename T, int D>
-NA_DEVICE void load_rows(const PackedArgs& p, const Span& sp, const T* g, int kh, long long r0, int n, int rows,
-                         float* s) {
+template <typename T, int D, int ROWS, int THREADS>
+NA_DEVICE void load_rows(const PackedArgs& p, const Span& sp, const T* g, int kh, long long r0, int n, float* s) {
   constexpr int VPR = D * sizeof(T) / 16;
-  for (int e = threadIdx.x; e < rows * VPR; e += kThreads) {
+#pragma unroll 4
+  for (int e = threadIdx.x; e < ROWS * VPR; e += THREADS) {
     const int r = e / VPR, v = e % VPR;
     const bool live = r < n;
     const long long rr = live ? r0 + r : r0;
     const long long at = ((long long)sp.q0 + rr / p.group) * p.hq + kh * p.group + rr % p.group;
-    load_vec<T, D>(g + at * D, s + r * Tile<D>::LD, v, live);
+    load_vec<T>(g + at * D, s + r * Tile<D>::LD, v, live);
   }
 }
-template <typename T, int D>
+template <typename T, int D, int THREADS>
 NA_DEVICE void load_keys(const PackedArgs& p, const Span& sp, const T* g, int kh, int k0, int n, float* s) {
   constexpr int VPR = D * sizeof(T) / 16;
-  for (int e = threadIdx.x; e < kKeys * VPR; e += kThreads) {
+#pragma unroll 4
+  for (int e = threadIdx.x; e < kKeys * VPR; e += THREADS) {
     const int j = e / VPR, v = e % VPR;
     const bool live = j < n;
     const long long at = ((long long)sp.k0 + (live ? k0 + j : k0)) * p.hk + kh;
-    load_vec<T, D>(g + at * D, s + j * Tile<D>::LD, v, live);
+    load_vec<T>(g + at * D, s + j * Tile<D>::LD, v, live);
   }
 }
 
-// c[r][j] = a row (ty R + r) . b row (tx + 8 j) of two staged tiles
+// c[r][j] = a row (ty R + r) . b row (tx + 8 j) of two staged tiles.  Even and
+// odd columns are summed apart, two of them an instruction.
 template <int D, int R>
 NA_DEVICE void dot_patch(const float* a, const float* b, int ty, int tx, float (&c)[R][8]) {
   constexpr int LD = Tile<D>::LD;
+  float even[R][8], odd[R][8];
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) c[r][j] = 0.f;
-#pragma unroll 4
+    for (int j = 0; j < 8; ++j) even[r][j] = odd[r][j] = 0.f;
+#pragma unroll 2
   for (int d = 0; d < D; d += 4) {
     float4 x[R];
 #pragma unroll
@@ -96,23 +114,26 @@ NA_DEVICE void dot_patch(const float* a, const float* b, int ty, int tx, float (
       const float4 y = *reinterpret_cast<const float4*>(b + (tx + 8 * j) * LD + d);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        c[r][j] = fmaf(x[r].x, y.x, c[r][j]);
-        c[r][j] = fmaf(x[r].y, y.y, c[r][j]);
-        c[r][j] = fmaf(x[r].z, y.z, c[r][j]);
-        c[r][j] = fmaf(x[r].w, y.w, c[r][j]);
+        sm100::fma2(even[r][j], odd[r][j], x[r].x, x[r].y, y.x, y.y, even[r][j], odd[r][j]);
+        sm100::fma2(even[r][j], odd[r][j], x[r].z, x[r].w, y.z, y.w, even[r][j], odd[r][j]);
       }
     }
   }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c[r][j] = even[r][j] + odd[r][j];
 }
 
-// acc[r][.] += w[ty R + r][j] * b[j][this thread's columns] for j in [0, n)
-// with j inside row r's [lo, hi)
-template <int D, int R, int WLD>
-NA_DEVICE void weighted_sum(const float* w, const float* b, int ty, int tx, int n, const int (&lo)[R],
-                            const int (&hi)[R], float (&acc)[R][Tile<D>::CPT]) {
+// acc[r][.] += w[ty R + r][j] * b[j][this thread's columns] for j inside row
+// r's [lo, hi), which lie in [0, kKeys).  A thread's rows are neighbours and
+// their ranges all but alike, so the keys go by fours, and only fours that some
+// row sees in part are asked key by key.
+template <int D, int R>
+NA_DEVICE void weighted_sum(const float* w, const float* b, int ty, int tx, const int (&lo)[R], const int (&hi)[R],
+                            float (&acc)[R][Tile<D>::CPT]) {
   constexpr int LD = Tile<D>::LD, CPT = Tile<D>::CPT, CV = Tile<D>::CV;
-  for (int j = 0; j < n; ++j) {
-    float v[CPT];
+  auto columns = [&](int j, float (&v)[CPT]) {
 #pragma unroll
     for (int c = 0; c < CPT / CV; ++c) {
       const float* from = b + j * LD + c * 8 * CV + tx * CV;
@@ -124,12 +145,42 @@ NA_DEVICE void weighted_sum(const float* w, const float* b, int ty, int tx, int 
         v[0] = f.x, v[1] = f.y;
       }
     }
+  };
+  auto add = [&](int r, float x, const float (&v)[CPT]) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const float x = w[(ty * R + r) * WLD + j];
-      if (j >= lo[r] && j < hi[r])
+    for (int c = 0; c < CPT; c += 2)
+      sm100::fma2(acc[r][c], acc[r][c + 1], x, x, v[c], v[c + 1], acc[r][c], acc[r][c + 1]);
+  };
+  int first = kKeys, last = 0, all_lo = 0, all_hi = kKeys;  // seen by some row; seen by all
 #pragma unroll
-        for (int c = 0; c < CPT; ++c) acc[r][c] = fmaf(x, v[c], acc[r][c]);
+  for (int r = 0; r < R; ++r) {
+    if (lo[r] < hi[r]) {
+      first = min(first, lo[r]);
+      last = max(last, hi[r]);
+    }
+    all_lo = max(all_lo, lo[r]);
+    all_hi = min(all_hi, hi[r]);
+  }
+  for (int j = first & ~3; j < last; j += 4) {
+    float4 x[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) x[r] = *reinterpret_cast<const float4*>(w + (ty * R + r) * kLdW + j);
+    float v[CPT];
+    if (j >= all_lo && j + 4 <= all_hi) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        columns(j + i, v);
+#pragma unroll
+        for (int r = 0; r < R; ++r) add(r, (&x[r].x)[i], v);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        columns(j + i, v);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          if (j + i >= lo[r] && j + i < hi[r]) add(r, (&x[r].x)[i], v);
+      }
     }
   }
 }
@@ -141,14 +192,14 @@ NA_DEVICE void store_cols(T* g, int tx, const float (&acc)[Tile<D>::CPT], float 
   for (int c = 0; c < CPT; ++c) g[(c / CV) * 8 * CV + tx * CV + c % CV] = from_f<T>(acc[c] * f);
 }
 
-template <int D, int R> constexpr int fwd_smem() {
-  return (16 * R * Tile<D>::LD + 2 * kKeys * Tile<D>::LD + 16 * R * (kKeys + 1)) * (int)sizeof(float);
+template <int D, int ROWS> constexpr int fwd_smem() {
+  return (ROWS * Tile<D>::LD + 2 * kKeys * Tile<D>::LD + ROWS * kLdW) * (int)sizeof(float);
 }
 
 // ----------------------------------------------------------------- forward
-template <typename T, int D, int R>
-__global__ void __launch_bounds__(kThreads) packed_forward_simt_kernel(PackedArgs p) {
-  constexpr int ROWS = 16 * R, LD = Tile<D>::LD, CPT = Tile<D>::CPT;
+template <typename T, int D, int R, int THREADS>
+__global__ void __launch_bounds__(THREADS) packed_forward_simt_kernel(PackedArgs p) {
+  constexpr int ROWS = THREADS / 8 * R, LD = Tile<D>::LD, CPT = Tile<D>::CPT;
   extern __shared__ __align__(16) float sm[];
   float* Qs = sm;
   float* Ks = Qs + ROWS * LD;
@@ -159,8 +210,9 @@ __global__ void __launch_bounds__(kThreads) packed_forward_simt_kernel(PackedArg
   const float sl2 = p.scale * kLog2e;
   int s;
   long long idx;
-  const bool split = p.piece_keys > 0;
-  if (split)
+  // keys in pieces of one length, or a share of every sequence's a plane
+  const bool split = p.max_pieces > 1, by_keys = p.piece_keys > 0;
+  if (by_keys)
     find_part(p.cu_k, p.nseq, p.total_k, 1, p.piece_keys, blockIdx.x, &s, &idx);
   else
     find_part(p.cu_q, p.nseq, p.total_q, p.group, ROWS, blockIdx.x, &s, &idx);
@@ -169,10 +221,15 @@ __global__ void __launch_bounds__(kThreads) packed_forward_simt_kernel(PackedArg
   const long long all_rows = (long long)sp.nq * p.group;
   int piece0 = 0, piece1 = sp.nk;
   long long t0 = idx, t1 = idx + 1;
+  int piece = 0;
   if (split) {
-    if (idx >= p.max_pieces || idx * p.piece_keys >= sp.nk) return;
-    piece0 = (int)idx * p.piece_keys;
-    piece1 = min(piece0 + p.piece_keys, sp.nk);
+    const int len = piece_length(p, sp);
+    if (by_keys && (idx >= p.max_pieces || idx * len >= sp.nk)) return;
+    piece = by_keys ? (int)idx : (int)blockIdx.z;
+    piece0 = (int)min((long long)piece * len, (long long)sp.nk);
+    piece1 = min(piece0 + len, sp.nk);
+  }
+  if (by_keys) {
     t0 = 0;
     t1 = (all_rows + ROWS - 1) / ROWS;
   }
@@ -192,7 +249,13 @@ __global__ void __launch_bounds__(kThreads) packed_forward_simt_kernel(PackedArg
       if (row >= n) hi[r] = lo[r];
     }
     __syncthreads();
-    load_rows<T, D>(p, sp, (const T*)p.q, kh, r0, n, ROWS, Qs);
+    load_rows<T, D, ROWS, THREADS>(p, sp, (const T*)p.q, kh, r0, n, Qs);
+    auto ask = [&](const void* g, int k0, float* to) {
+      if (k0 < ke) load_keys<T, D, THREADS>(p, sp, (const T*)g, kh, k0, min(kKeys, ke - k0), to);
+      end_copies();
+    };
+    ask(p.k, kb, Ks);
+    ask(p.v, kb, Vs);
     float m[R], l[R], acc[R][CPT];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -203,16 +266,16 @@ __global__ void __launch_bounds__(kThreads) packed_forward_simt_kernel(PackedArg
     }
     for (int k0 = kb; k0 < ke; k0 += kKeys) {
       const int nk = min(kKeys, ke - k0);
-      __syncthreads();
-      load_keys<T, D>(p, sp, (const T*)p.k, kh, k0, nk, Ks);
-      load_keys<T, D>(p, sp, (const T*)p.v, kh, k0, nk, Vs);
+      wait_copies<1>();  // K is here, V may be on its way
       __syncthreads();
       float sc[R][8];
       dot_patch<D, R>(Qs, Ks, ty, tx, sc);
+      __syncthreads();
+      ask(p.k, k0 + kKeys, Ks);
       int tlo[R], thi[R];
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        tlo[r] = lo[r] - k0;
+        tlo[r] = max(lo[r] - k0, 0);
         thi[r] = min(hi[r] - k0, nk);
         float mx = m[r];
 #pragma unroll
@@ -230,16 +293,20 @@ __global__ void __launch_bounds__(kThreads) packed_forward_simt_kernel(PackedArg
         for (int j = 0; j < 8; ++j) {
           const float e = exp2f(fmaf(sc[r][j], sl2, -ref));
           sum += e;
-          Ps[(ty * R + r) * (kKeys + 1) + tx + 8 * j] = e;
+          Ps[(ty * R + r) * kLdW + tx + 8 * j] = e;
         }
         l[r] = fmaf(l[r], f, sum);
         m[r] = mx;
 #pragma unroll
         for (int c = 0; c < CPT; ++c) acc[r][c] *= f;
       }
-      __syncwarp();
-      weighted_sum<D, R, kKeys + 1>(Ps, Vs, ty, tx, nk, tlo, thi, acc);
+      wait_copies<1>();
+      __syncthreads();
+      weighted_sum<D, R>(Ps, Vs, ty, tx, tlo, thi, acc);
+      __syncthreads();
+      ask(p.v, k0 + kKeys, Vs);
     }
+    wait_copies<0>();
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       float sum = l[r];
@@ -254,7 +321,7 @@ __global__ void __launch_bounds__(kThreads) packed_forward_simt_kernel(PackedArg
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       const float lse = sum == 0.f ? -INFINITY : fmaf(m[r], p.scale, log2f(sum) * kLn2);
       if (split) {
-        const long long at = (idx * p.total_q + i) * p.hq + head;
+        const long long at = ((long long)piece * p.total_q + i) * p.hq + head;
         store_cols<float, D, R>(p.part_o + at * D, tx, acc[r], inv);
         if (tx == 0) p.part_lse[at] = lse;
       } else {
@@ -334,7 +401,7 @@ template <typename T, int D> __global__ void __launch_bounds__(256) packed_terms
 }
 
 template <int D> constexpr int bwd_smem() {
-  return (4 * kKeys * Tile<D>::LD + 2 * kKeys * (kKeys + 1) + 2 * kKeys) * (int)sizeof(float);
+  return (4 * kKeys * Tile<D>::LD + 2 * kKeys * kLdW + 2 * kKeys) * (int)sizeof(float);
 }
 
 // lse (in units of log2) and delta of the staged rows
@@ -351,17 +418,19 @@ NA_DEVICE void load_row_terms(const PackedArgs& p, const Span& sp, int kh, long 
   }
 }
 
+constexpr int kBwdThreads = 256;
+
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) packed_dkdv_simt_kernel(PackedArgs p) {
-  constexpr int R = 4, LD = Tile<D>::LD, CPT = Tile<D>::CPT, WLD = kKeys + 1;
+__global__ void __launch_bounds__(kBwdThreads, D == 128 ? 1 : 2) packed_dkdv_simt_kernel(PackedArgs p) {
+  constexpr int R = 2, LD = Tile<D>::LD, CPT = Tile<D>::CPT;
   extern __shared__ __align__(16) float sm[];
   float* Ks = sm;
   float* Vs = Ks + kKeys * LD;
   float* Qs = Vs + kKeys * LD;
   float* Os = Qs + kKeys * LD;
   float* Ps = Os + kKeys * LD;
-  float* Ss = Ps + kKeys * WLD;
-  float* lse = Ss + kKeys * WLD;
+  float* Ss = Ps + kKeys * kLdW;
+  float* lse = Ss + kKeys * kLdW;
   float* delta = lse + kKeys;
   const int ty = threadIdx.x / 8, tx = threadIdx.x % 8;
   const int kh = blockIdx.y;
@@ -373,8 +442,8 @@ __global__ void __launch_bounds__(kThreads) packed_dkdv_simt_kernel(PackedArgs p
   const Span sp = span_of(p, s);
   if (idx * kKeys >= sp.nk) return;
   const int j0 = (int)idx * kKeys, nk = min(kKeys, sp.nk - j0);
-  load_keys<T, D>(p, sp, (const T*)p.k, kh, j0, nk, Ks);
-  load_keys<T, D>(p, sp, (const T*)p.v, kh, j0, nk, Vs);
+  load_keys<T, D, kBwdThreads>(p, sp, (const T*)p.k, kh, j0, nk, Ks);
+  load_keys<T, D, kBwdThreads>(p, sp, (const T*)p.v, kh, j0, nk, Vs);
   long long lo[R], hi[R];  // rows that see this thread's keys
   int a, b;
 #pragma unroll
@@ -392,12 +461,18 @@ __global__ void __launch_bounds__(kThreads) packed_dkdv_simt_kernel(PackedArgs p
   int unused, first, last;
   seen_by(p, sp, j0, &first, &unused);
   seen_by(p, sp, j0 + nk - 1, &unused, &last);
-  for (long long r0 = (long long)first * p.group; r0 < (long long)last * p.group; r0 += kKeys) {
-    const int n = (int)min((long long)kKeys, (long long)last * p.group - r0);
+  // this block's piece of the rows that see its keys
+  const long long begin = (long long)first * p.group, tiles = ((long long)last * p.group - begin + kKeys - 1) / kKeys;
+  const long long per = (tiles + gridDim.z - 1) / gridDim.z * kKeys;
+  const long long from = begin + blockIdx.z * per, to = min(from + per, (long long)last * p.group);
+  for (long long r0 = from; r0 < to; r0 += kKeys) {
+    const int n = (int)min((long long)kKeys, to - r0);
     __syncthreads();
-    load_rows<T, D>(p, sp, (const T*)p.q, kh, r0, n, kKeys, Qs);
-    load_rows<T, D>(p, sp, (const T*)p.dout, kh, r0, n, kKeys, Os);
+    load_rows<T, D, kKeys, kBwdThreads>(p, sp, (const T*)p.q, kh, r0, n, Qs);
+    load_rows<T, D, kKeys, kBwdThreads>(p, sp, (const T*)p.dout, kh, r0, n, Os);
+    end_copies();
     load_row_terms(p, sp, kh, r0, n, lse, delta);
+    wait_copies<0>();
     __syncthreads();
     float sc[R][8], dp[R][8];
     dot_patch<D, R>(Ks, Qs, ty, tx, sc);
@@ -411,34 +486,41 @@ __global__ void __launch_bounds__(kThreads) packed_dkdv_simt_kernel(PackedArgs p
       for (int j = 0; j < 8; ++j) {
         const int row = tx + 8 * j;
         const float e = exp2f(fmaf(sc[r][j], sl2, -lse[row]));
-        Ps[(ty * R + r) * WLD + row] = e;
-        Ss[(ty * R + r) * WLD + row] = e * (dp[r][j] - delta[row]);
+        Ps[(ty * R + r) * kLdW + row] = e;
+        Ss[(ty * R + r) * kLdW + row] = e * (dp[r][j] - delta[row]);
       }
     }
     __syncwarp();
-    weighted_sum<D, R, WLD>(Ps, Os, ty, tx, n, tlo, thi, dv);
-    weighted_sum<D, R, WLD>(Ss, Qs, ty, tx, n, tlo, thi, dk);
+    weighted_sum<D, R>(Ps, Os, ty, tx, tlo, thi, dv);
+    weighted_sum<D, R>(Ss, Qs, ty, tx, tlo, thi, dk);
   }
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int j = ty * R + r;
     if (j >= nk) continue;
     const long long at = ((long long)(sp.k0 + j0 + j) * p.hk + kh) * D;
-    store_cols<T, D, R>((T*)p.dk + at, tx, dk[r], p.scale);
-    store_cols<T, D, R>((T*)p.dv + at, tx, dv[r], 1.f);
+    if (gridDim.z > 1) {
+      const long long all = (long long)p.total_k * p.hk * D;
+      float* part = p.part_o + blockIdx.z * 2 * all + at;
+      store_cols<float, D, R>(part, tx, dv[r], 1.f);
+      store_cols<float, D, R>(part + all, tx, dk[r], p.scale);
+    } else {
+      store_cols<T, D, R>((T*)p.dk + at, tx, dk[r], p.scale);
+      store_cols<T, D, R>((T*)p.dv + at, tx, dv[r], 1.f);
+    }
   }
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) packed_dq_simt_kernel(PackedArgs p) {
-  constexpr int R = 4, LD = Tile<D>::LD, CPT = Tile<D>::CPT, WLD = kKeys + 1, ROWS = 64;
+__global__ void __launch_bounds__(kBwdThreads, D == 128 ? 1 : 2) packed_dq_simt_kernel(PackedArgs p) {
+  constexpr int R = 2, LD = Tile<D>::LD, CPT = Tile<D>::CPT, ROWS = 64;
   extern __shared__ __align__(16) float sm[];
   float* Ks = sm;
   float* Vs = Ks + kKeys * LD;
   float* Qs = Vs + kKeys * LD;
   float* Os = Qs + kKeys * LD;
   float* Ss = Os + kKeys * LD;
-  float* lse = Ss + 2 * kKeys * WLD;
+  float* lse = Ss + 2 * kKeys * kLdW;
   float* delta = lse + kKeys;
   const int ty = threadIdx.x / 8, tx = threadIdx.x % 8;
   const int kh = blockIdx.y;
@@ -451,8 +533,8 @@ __global__ void __launch_bounds__(kThreads) packed_dq_simt_kernel(PackedArgs p) 
   const long long all_rows = (long long)sp.nq * p.group, r0 = idx * ROWS;
   if (r0 >= all_rows) return;
   const int n = (int)min((long long)ROWS, all_rows - r0);
-  load_rows<T, D>(p, sp, (const T*)p.q, kh, r0, n, ROWS, Qs);
-  load_rows<T, D>(p, sp, (const T*)p.dout, kh, r0, n, ROWS, Os);
+  load_rows<T, D, ROWS, kBwdThreads>(p, sp, (const T*)p.q, kh, r0, n, Qs);
+  load_rows<T, D, ROWS, kBwdThreads>(p, sp, (const T*)p.dout, kh, r0, n, Os);
   load_row_terms(p, sp, kh, r0, n, lse, delta);
   int lo[R], hi[R], kb, ke, unused;
   visible(p, sp, (int)(r0 / p.group), &kb, &unused);
@@ -471,8 +553,10 @@ __global__ void __launch_bounds__(kThreads) packed_dq_simt_kernel(PackedArgs p) 
   for (int k0 = kb; k0 < ke; k0 += kKeys) {
     const int nk = min(kKeys, ke - k0);
     __syncthreads();
-    load_keys<T, D>(p, sp, (const T*)p.k, kh, k0, nk, Ks);
-    load_keys<T, D>(p, sp, (const T*)p.v, kh, k0, nk, Vs);
+    load_keys<T, D, kBwdThreads>(p, sp, (const T*)p.k, kh, k0, nk, Ks);
+    load_keys<T, D, kBwdThreads>(p, sp, (const T*)p.v, kh, k0, nk, Vs);
+    end_copies();
+    wait_copies<0>();
     __syncthreads();
     float sc[R][8], dp[R][8];
     dot_patch<D, R>(Qs, Ks, ty, tx, sc);
@@ -480,15 +564,15 @@ __global__ void __launch_bounds__(kThreads) packed_dq_simt_kernel(PackedArgs p) 
     int tlo[R], thi[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      tlo[r] = lo[r] - k0;
+      tlo[r] = max(lo[r] - k0, 0);
       thi[r] = min(hi[r] - k0, nk);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        Ss[(ty * R + r) * WLD + tx + 8 * j] =
+        Ss[(ty * R + r) * kLdW + tx + 8 * j] =
             exp2f(fmaf(sc[r][j], sl2, -lse[ty * R + r])) * (dp[r][j] - delta[ty * R + r]);
     }
     __syncwarp();
-    weighted_sum<D, R, WLD>(Ss, Ks, ty, tx, nk, tlo, thi, dq);
+    weighted_sum<D, R>(Ss, Ks, ty, tx, tlo, thi, dq);
   }
 #pragma unroll
   for (int r = 0; r < R; ++r) {
@@ -507,18 +591,20 @@ template <typename K> cudaError_t with_smem(K kern, int bytes) {
 
 bool few_rows(const PackedArgs& p) { return (long long)p.total_q * p.group <= 16ll * p.nseq; }
 
-template <typename T, int D, int R> cudaError_t forward_r(const PackedArgs& p, cudaStream_t st) {
+template <typename T, int D, int R, int THREADS> cudaError_t forward_r(const PackedArgs& p, cudaStream_t st) {
+  constexpr int ROWS = THREADS / 8 * R;
   const long long blocks = p.piece_keys > 0 ? part_numbers(p.nseq, p.total_k, 1, p.piece_keys)
-                                            : part_numbers(p.nseq, p.total_q, p.group, 16 * R);
+                                            : part_numbers(p.nseq, p.total_q, p.group, ROWS);
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  auto kern = packed_forward_simt_kernel<T, D, R>;
-  cudaError_t e = with_smem(kern, fwd_smem<D, R>());
+  auto kern = packed_forward_simt_kernel<T, D, R, THREADS>;
+  cudaError_t e = with_smem(kern, fwd_smem<D, ROWS>());
   if (e != cudaSuccess) return e;
-  kern<<<dim3((unsigned)blocks, (unsigned)p.hk), kThreads, fwd_smem<D, R>(), st>>>(p);
+  const unsigned planes = p.piece_keys > 0 ? 1u : (unsigned)p.max_pieces;
+  kern<<<dim3((unsigned)blocks, (unsigned)p.hk, planes), THREADS, fwd_smem<D, ROWS>(), st>>>(p);
   return cudaGetLastError();
 }
 template <typename T, int D> cudaError_t forward_d(const PackedArgs& p, cudaStream_t st) {
-  return few_rows(p) ? forward_r<T, D, 1>(p, st) : forward_r<T, D, 4>(p, st);
+  return few_rows(p) ? forward_r<T, D, 1, 128>(p, st) : forward_r<T, D, 2, 128>(p, st);
 }
 template <typename T> cudaError_t forward_t(const PackedArgs& p, cudaStream_t st) {
   switch (p.d) {
@@ -529,15 +615,20 @@ template <typename T> cudaError_t forward_t(const PackedArgs& p, cudaStream_t st
   }
   return cudaErrorInvalidValue;
 }
+template <typename T> constexpr na_dtype dt_of() {
+  return sizeof(T) == 4 ? NA_F32 : std::is_same_v<T, __half> ? NA_F16 : NA_BF16;
+}
 template <typename T, int D> cudaError_t backward_d(const PackedArgs& p, cudaStream_t st) {
   const long long kb = part_numbers(p.nseq, p.total_k, 1, kKeys), qb = part_numbers(p.nseq, p.total_q, p.group, 64);
   if (kb > 0x7fffffffLL || qb > 0x7fffffffLL) return cudaErrorInvalidValue;
   cudaError_t e = with_smem(packed_dkdv_simt_kernel<T, D>, bwd_smem<D>());
   if (e == cudaSuccess) e = with_smem(packed_dq_simt_kernel<T, D>, bwd_smem<D>());
   if (e != cudaSuccess) return e;
-  packed_dkdv_simt_kernel<T, D><<<dim3((unsigned)kb, (unsigned)p.hk), kThreads, bwd_smem<D>(), st>>>(p);
-  packed_dq_simt_kernel<T, D><<<dim3((unsigned)qb, (unsigned)p.hk), kThreads, bwd_smem<D>(), st>>>(p);
-  return cudaGetLastError();
+  packed_dkdv_simt_kernel<T, D><<<dim3((unsigned)kb, (unsigned)p.hk, (unsigned)p.max_pieces), kBwdThreads, bwd_smem<D>(), st>>>(p);
+  packed_dq_simt_kernel<T, D><<<dim3((unsigned)qb, (unsigned)p.hk), kBwdThreads, bwd_smem<D>(), st>>>(p);
+  cudaError_t launched = cudaGetLastError();
+  if (launched == cudaSuccess && p.max_pieces > 1) launched = launch_packed_dkdv_join(p, dt_of<T>(), st);
+  return launched;
 }
 template <typename T> cudaError_t backward_t(const PackedArgs& p, cudaStream_t st) {
   switch (p.d) {
@@ -594,12 +685,12 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 // few rows shares a sequence's keys among 8 blocks by itself and cuts only
 // where sequences times heads are fewer than 19, which leaves SMs without a
 // block, and sequences are longer than 4096 keys on average, of which a block's
-// share takes longer than a second launch.  It and the CUDA-core kernel cut every sequence into pieces of one
-// length, as long as leaves about `want` blocks but not under 256 keys (each
-// piece's rows pay for writing and joining a float32 output), so that long
-// sequences make more pieces than short ones.  The tensor-core kernel cuts
-// every sequence into the same number of pieces of 512 keys at least, as its
-// grid counts row tiles.
+// share takes longer than a second launch.  It and the CUDA-core kernel for few
+// rows cut every sequence into pieces of one length, as long as leaves about
+// `want` blocks but not under 256 keys (each piece's rows pay for writing and
+// joining a float32 output), so that long sequences make more pieces than short
+// ones.  The kernels for many rows cut every sequence into the same number of
+// pieces of 512 keys at least, as their grids count row tiles.
 void packed_plan(PackedArgs* p, na_dtype dt) {
   constexpr long long kSms = 148, kMost = 256ll << 20;
   p->piece_keys = 0;
@@ -607,19 +698,19 @@ void packed_plan(PackedArgs* p, na_dtype dt) {
   const bool few = (long long)p->total_q * p->group <= 16ll * p->nseq;
   p->path = dt == NA_F32 || p->group > 128 || p->total_k == 0 ? kPathSimt : few ? kPathRows : kPathTc;
   const long long row_bytes = (long long)p->total_q * p->hq * (p->d + 1) * 4;
-  if (p->path == kPathTc) {
-    const int per = packed_row_tiles(p->d) * (128 / p->group);
-    const long long tiles = part_numbers(p->nseq, p->total_q, 1, per) * p->hk;
-    long long pieces = kSms / tiles;
+  if (p->path == kPathTc || !few) {
+    const bool tc = p->path == kPathTc;
+    const long long tiles = p->hk * (tc ? part_numbers(p->nseq, p->total_q, 1, packed_row_tiles(p->d) * (128 / p->group))
+                                        : part_numbers(p->nseq, p->total_q, p->group, 64));
+    long long pieces = (tc ? kSms : 2 * kSms) / tiles;
     if (pieces > p->total_k / p->nseq / 512) pieces = p->total_k / p->nseq / 512;
     while (pieces > 1 && pieces * row_bytes > kMost) --pieces;
     if (pieces > 1) p->max_pieces = (int)pieces;
     return;
   }
   if (p->path == kPathRows && ((long long)p->nseq * p->hk * 8 >= kSms || p->total_k / p->nseq <= 4096)) return;
-  const int rows = few ? 16 : 64;
   const long long want = (p->path == kPathRows ? 4 : 8) * kSms, least = 256;
-  const long long per_seq = ((long long)p->total_q * p->group / p->nseq + rows) / rows;  // row tiles, about
+  const long long per_seq = ((long long)p->total_q * p->group / p->nseq + 16) / 16;  // row tiles, about
   if (per_seq * p->nseq * p->hk >= 4 * kSms) return;
   long long keys = (long long)p->total_k * p->hk * per_seq / want;
   if (keys < least) keys = least;
@@ -646,12 +737,15 @@ void packed_backward_plan(PackedArgs* p, na_dtype dt) {
   constexpr long long kSms = 148, kMost = 512ll << 20;
   p->piece_keys = 0;
   p->max_pieces = 1;
-  p->path = dt == NA_F32 || p->group > 128 || p->total_k == 0 || p->total_q == 0 ? kPathSimt : kPathTc;
-  if (p->path != kPathTc) return;
-  const long long tiles = part_numbers(p->nseq, p->total_k, 1, 128) * p->hk;
-  const long long walk = (long long)p->total_q / p->nseq / (128 / p->group);  // row tiles of a key tile, about
+  const bool tc = !(dt == NA_F32 || p->group > 128 || p->total_k == 0 || p->total_q == 0);
+  p->path = tc ? kPathTc : kPathSimt;
+  if (p->total_k == 0 || p->total_q == 0) return;
+  const long long tiles = part_numbers(p->nseq, p->total_k, 1, tc ? 128 : kKeys) * p->hk;
+  // row tiles of a key tile, about
+  const long long walk = tc ? (long long)p->total_q / p->nseq / (128 / p->group)
+                            : (long long)p->total_q * p->group / p->nseq / 64;
   long long pieces = (5 * kSms / 2 + tiles - 1) / tiles;
-  if (pieces > walk / 8) pieces = walk / 8;
+  if (pieces > walk / (tc ? 8 : 4)) pieces = walk / (tc ? 8 : 4);
   if (pieces > 8) pieces = 8;
   while (pieces > 1 && pieces * p->total_k * p->hk * p->d * 8 > kMost) --pieces;
   if (pieces > 1) p->max_pieces = (int)pieces;

@@ -493,7 +493,11 @@ template <typename T> __global__ void __launch_bounds__(256) packed_dkdv_join_ke
     const float4 v = *reinterpret_cast<const float4*>(from + (long long)z * 2 * per * 8 + 4);
     f[0] += u.x, f[1] += u.y, f[2] += u.z, f[3] += u.w, f[4] += v.x, f[5] += v.y, f[6] += v.z, f[7] += v.w;
   }
-  store_run<T, 8>((T*)(which ? p.dk : p.dv) + e * 8, f);
+  T* to = (T*)(which ? p.dk : p.dv) + e * 8;
+  if constexpr (sizeof(T) == 4)
+    store_run<8>(to, f);
+  else
+    store_run<T, 8>(to, f);
 }
 
 // ---------------------------------------------------------------------- dq
@@ -784,12 +788,7 @@ template <typename T, int D> cudaError_t launch(const PackedArgs& p, cudaStream_
   packed_dkdv_tc_kernel<T, D>
       <<<(unsigned)(kb * p.hk * p.max_pieces), C::THREADS, C::SMEM_ASKED, st>>>(mq, mo, mk, mv, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (p.max_pieces > 1) {
-    const long long blocks = ((long long)p.total_k * p.hk * (D / 8) + 255) / 256;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    packed_dkdv_join_kernel<T><<<dim3((unsigned)blocks, 2), 256, 0, st>>>(p);
-  }
-  return cudaGetLastError();
+  return p.max_pieces > 1 ? launch_packed_dkdv_join(p, bf16 ? NA_BF16 : NA_F16, st) : cudaSuccess;
 }
 template <typename T> cudaError_t launch_d(const PackedArgs& p, cudaStream_t st) {
   switch (p.d) {
@@ -802,6 +801,19 @@ template <typename T> cudaError_t launch_d(const PackedArgs& p, cudaStream_t st)
 }
 
 }  // namespace
+
+cudaError_t launch_packed_dkdv_join(const PackedArgs& p, na_dtype dt, cudaStream_t st) {
+  const long long blocks = ((long long)p.total_k * p.hk * (p.d / 8) + 255) / 256;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const dim3 grid((unsigned)blocks, 2);
+  if (dt == NA_F32)
+    packed_dkdv_join_kernel<float><<<grid, 256, 0, st>>>(p);
+  else if (dt == NA_F16)
+    packed_dkdv_join_kernel<__half><<<grid, 256, 0, st>>>(p);
+  else
+    packed_dkdv_join_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(p);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_packed_backward_tc(const PackedArgs& p, na_dtype dt, cudaStream_t st) {
   return dt == NA_F16 ? launch_d<__half>(p, st) : launch_d<__nv_bfloat16>(p, st);
