@@ -11,8 +11,7 @@
 // memory's 128 bytes a clock bound it: 10 loads of 4 clocks for 64 FMAs.  Rows
 // of 32 rather than 64, in 128 threads, leave more blocks to an SM: 700 + 33 +
 // 512 + 257 rows of 8 heads, d = 64, window 200, take 39 us, against 54 in
-// blocks of 64 rows and 256 threads; only a batch without a mask that fills
-// the device by far (3000 rows of 16 heads) gains 3% from the latter.
+// blocks of 64 rows and 256 threads.
 //
 // Backward.  P and dS are recomputed from the rows' log-sum-exp, once with a
 // block owning 64 keys (dk, dv) and once with a block owning 64 rows (dq): two
@@ -701,7 +700,7 @@ void packed_plan(PackedArgs* p, na_dtype dt) {
   if (p->path == kPathTc || !few) {
     const bool tc = p->path == kPathTc;
     const long long tiles = p->hk * (tc ? part_numbers(p->nseq, p->total_q, 1, packed_row_tiles(p->d) * (128 / p->group))
-                                        : part_numbers(p->nseq, p->total_q, p->group, 64));
+                                        : part_numbers(p->nseq, p->total_q, p->group, 32));
     long long pieces = (tc ? kSms : 2 * kSms) / tiles;
     if (pieces > p->total_k / p->nseq / 512) pieces = p->total_k / p->nseq / 512;
     while (pieces > 1 && pieces * row_bytes > kMost) --pieces;

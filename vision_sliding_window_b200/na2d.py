@@ -339,7 +339,22 @@ def _bytes_for(name, *sizes) -> int:
     return int(getattr(load_library(), name)(*sizes))
 
 
+def _alike(t, where, dtype, shape) -> bool:
+    """What _need_all and _need_shape ask of one tensor, without words."""
+    return t.get_device() == where and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+
+
 def _packed_dims(q, k, v, cu_q, cu_k, len_k):
+    where, dtype = q.get_device(), q.dtype
+    if (where >= 0 and dtype in _DT and q.dim() == 3 and k.dim() == 3 and cu_q.dim() == 1 and cu_q.numel() > 0
+            and q.is_contiguous() and k.shape[2] == q.shape[2]):
+        ends, i32 = cu_q.shape, torch.int32
+        if (_alike(k, where, dtype, k.shape) and _alike(v, where, dtype, k.shape) and _alike(cu_q, where, i32, ends)
+                and _alike(cu_k, where, i32, ends) and (len_k is None or _alike(len_k, where, i32, (ends[0] - 1,)))):
+            total_q, heads_q, d = q.shape
+            total_k, heads_k, _ = k.shape
+            return ends[0] - 1, total_q, total_k, heads_q, heads_k, d
+    # something is wrong: say what
     _need(q, "q")
     if q.dtype not in _DT:
         raise ValueError(f"q must be float32, float16 or bfloat16, got {q.dtype}")
@@ -350,12 +365,9 @@ def _packed_dims(q, k, v, cu_q, cu_k, len_k):
     _need_shape(v, "v", k.shape)
     if cu_q.dim() != 1 or cu_q.numel() < 1:
         raise ValueError("cu_q must be [nseq + 1]")
-    nseq = cu_q.numel() - 1
-    _need_shape(cu_k, "cu_k", (nseq + 1,))
-    _need_shape(len_k, "len_k", (nseq,))
-    if k.shape[2] != q.shape[2]:
-        raise ValueError(f"k and v must have q's head size {q.shape[2]}, got {k.shape[2]}")
-    return nseq, int(q.shape[0]), int(k.shape[0]), int(q.shape[1]), int(k.shape[1]), int(q.shape[2])
+    _need_shape(cu_k, "cu_k", cu_q.shape)
+    _need_shape(len_k, "len_k", (cu_q.numel() - 1,))
+    raise ValueError(f"k and v must have q's head size {q.shape[2]}, got {k.shape[2]}")
 
 
 def packed_forward(q, k, v, cu_q, cu_k, len_k=None, causal: bool = False, window: int = 0, scale=None, out=None,
@@ -371,14 +383,21 @@ def packed_forward(q, k, v, cu_q, cu_k, len_k=None, causal: bool = False, window
     that this call allocates holds there is not defined."""
     dims = _packed_dims(q, k, v, cu_q, cu_k, len_k)
     nseq, tq, _, hq, _, d = dims
-    out = torch.empty_like(q) if out is None else out
-    lse = torch.empty((hq, tq), device=q.device, dtype=torch.float32) if lse is None else lse
-    _need_all(q, q.dtype, out=out)
-    _need_all(q, torch.float32, lse=lse)
-    _need_shape(out, "out", q.shape)
-    _need_shape(lse, "lse", (hq, tq))
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need_all(q, q.dtype, out=out)
+        _need_shape(out, "out", q.shape)
+    if lse is None:
+        lse = torch.empty((hq, tq), device=q.device, dtype=torch.float32)
+    else:
+        _need_all(q, torch.float32, lse=lse)
+        _need_shape(lse, "lse", (hq, tq))
     dt = _DT[q.dtype]
-    workspace, size = _workspace(workspace, _bytes_for("na_packed_workspace_bytes", *dims, dt), q)
+    need = _bytes_for("na_packed_workspace_bytes", *dims, dt)
+    size = 0
+    if need or workspace is not None:
+        workspace, size = _workspace(workspace, need, q)
     _enqueue(q, "na_packed_forward", (q, k, v, cu_q, cu_k, len_k, out, lse, workspace), size, *dims, int(causal),
              int(window), d ** -0.5 if scale is None else float(scale), dt)
     return out, lse
@@ -410,6 +429,21 @@ def packed_backward(q, k, v, out, lse, dout, cu_q, cu_k, causal: bool = False, w
 
 def _norm_dims(x, o, post, post_w, post_b, gate, w, b):
     """rows, C and gates of a norm's tensors; x is [..., C]."""
+    where, dtype, shape = x.get_device(), x.dtype, x.shape
+    if where >= 0 and dtype in _DT and len(shape) > 0 and x.is_contiguous():
+        C = shape[-1]
+        one = (C,)
+        if ((o is None or _alike(o, where, dtype, shape)) and (w is None or _alike(w, where, dtype, one))
+                and (b is None or _alike(b, where, dtype, one))
+                and (post_w is None or post and _alike(post_w, where, dtype, one))
+                and (post_b is None or post and _alike(post_b, where, dtype, one))
+                and (o is not None or not post and gate is None)):
+            rows = x.numel() // C if C else 0
+            if gate is None:
+                return rows, C, 0
+            if gate.dim() in (1, 2) and gate.shape[-1] == C and _alike(gate, where, dtype, gate.shape):
+                return rows, C, gate.numel() // C if C else 0
+    # something is wrong: say what
     _need(x, "x")
     if x.dtype not in _DT:
         raise ValueError(f"x must be float32, float16 or bfloat16, got {x.dtype}")
@@ -420,14 +454,11 @@ def _norm_dims(x, o, post, post_w, post_b, gate, w, b):
     _need_shape(o, "o", x.shape)
     for t, n in ((post_w, "post_w"), (post_b, "post_b"), (w, "w"), (b, "b")):
         _need_shape(t, n, (C,))
-    if gate is not None and (gate.dim() not in (1, 2) or gate.shape[-1] != C):
-        raise ValueError("gate must be [C] or [gates, C]")
     if o is None and (post or gate is not None):
         raise ValueError("post and gate act on o, which is missing")
     if not post and (post_w is not None or post_b is not None):
         raise ValueError("post_w and post_b need post=True")
-    gates = 0 if gate is None else int(gate.numel() // C) if C else 0
-    return (int(x.numel() // C) if C else 0), C, gates
+    raise ValueError("gate must be [C] or [gates, C]")
 
 
 def norm_forward(x, w=None, b=None, o=None, post: bool = False, post_w=None, post_b=None, gate=None,
@@ -444,13 +475,14 @@ def norm_forward(x, w=None, b=None, o=None, post: bool = False, post_w=None, pos
         raise ValueError("norm=False takes o, and neither w, b nor h")
     if o is None and y is not None:
         raise ValueError("without o, y is x: there is none to write")
-    if o is not None:
-        y = torch.empty_like(x) if y is None else y
-    if norm:
-        h = torch.empty_like(x) if h is None else h
-    _need_all(x, x.dtype, y=y, h=h)
-    _need_shape(y, "y", x.shape)
-    _need_shape(h, "h", x.shape)
+    for t, name in ((y, "y"), (h, "h")):
+        if t is not None:
+            _need_all(x, x.dtype, **{name: t})
+            _need_shape(t, name, x.shape)
+    if o is not None and y is None:
+        y = torch.empty_like(x)
+    if norm and h is None:
+        h = torch.empty_like(x)
     _enqueue(x, "na_norm_forward", (x, o, post_w, post_b, gate, w, b, y, h), rows, C, gates, int(rms), int(post),
              float(eps), float(scale), _DT[x.dtype])
     return (x if o is None else y), h
