@@ -121,6 +121,23 @@ def test_rows_far_from_zero_and_constant_rows(dtype, mean, rms):
         plain64.check(name, getattr(got, name), t, tol[name])
 
 
+@pytest.mark.parametrize("C", [64, 333, 768, 4096, 8188])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rows_that_begin_far_from_their_means(dtype, C):
+    x, kw, dy, dh = make(40, C, 2, True, True, dtype, seed=C)
+    x[::3, :8] += 1000.0
+    kw["o"][1::3, :8] -= 500.0
+    x[5, 0] = 3e4
+    y, h = na2d.norm_forward(x, **kw)
+    (wy, wh), (ty, th) = plain64.norm_forward(x, **kw)
+    plain64.check("y", y, wy, ty)
+    plain64.check("h", h, wh, th)
+    got = na2d.norm_backward(x, dh, dy, **kw)
+    want, tol = plain64.norm_backward(x, dh, dy, **kw)
+    for name, t in want.items():
+        plain64.check(name, getattr(got, name), t, tol[name])
+
+
 def test_in_place():
     x, kw, dy, dh = make(33, 768, 1, True, True, "bf16", seed=9)
     y, h = na2d.norm_forward(x, **kw)

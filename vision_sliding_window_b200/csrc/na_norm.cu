@@ -9,7 +9,7 @@
 // A row lives in registers between its one read and its one write, so the
 // forward pass moves x, o, y and h once each and the backward pass y, o, dy,
 // dh, dx and do once each.  HBM would bound both (82 us and 61 us at 16387 and
-// 8168 rows of 4096, bf16, both norms and a gate); what they take, 106 and 148
+// 8168 rows of 4096, bf16, both norms and a gate); what they take, 105 and 156
 // us, goes to instruction issue and to the waits of the reductions between a
 // row's steps.  So arithmetic is in pairs (two float32 an instruction), weights
 // stay in registers, rows that fill their threads have kernels without a
@@ -19,8 +19,7 @@
 // Statistics are float32.  Forward: the mean first, then the mean square of the
 // deviations from it, which is exact to rounding whatever the mean is, as "sum
 // of squares minus squared sum" is not.  Backward: sums over differences from a
-// few of the row's own values, see backward_row; float32 rows take the mean
-// itself first.
+// few of the row's own values, see backward_row.
 #include <type_traits>
 
 #include "na2d_common.cuh"
@@ -95,8 +94,10 @@ struct Reducer {
   template <bool BLOCK, int K> NA_DEVICE void sum(float (&v)[K]) {
     if constexpr (!BLOCK) {
 #pragma unroll
-      for (int k = 0; k < K; ++k)
-        for (int o = 1; o < lanes; o <<= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+      for (int o = 1; o < 32; o <<= 1)
+        if (o < lanes)
+#pragma unroll
+          for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
     } else {
       constexpr int P = K > 4 ? 8 : K > 2 ? 4 : K;  // a power of two
       const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -499,7 +500,9 @@ template <typename T, int VEC, int NV, bool ONE, bool kHeld> struct BackwardVect
 // one reduction: variance = mean square - squared mean of them.  With `first`
 // the mean of m of the row's own C values this loses at most a factor 1 + C / m
 // to cancellation, as those m values alone make the variance m / C times their
-// mean's squared distance; mostly it loses nothing.
+// mean's squared distance; mostly it loses nothing.  In wide 16-bit rows m is
+// 64, so that C = 8192 loses 7 bits of float32 at worst; other rows take the
+// mean itself.
 //
 // ONE (one gate row in all of the block's rows): the gate is a factor of whole
 // sums, so that sums.pw and sums.pb gather dx . m and dx (dx . o in sums.pw
@@ -741,21 +744,15 @@ __global__ void __launch_bounds__(BLOCK ? 512 : 256, BLOCK ? 1 : 2) norm_backwar
       if (next < r1) ask(next + sub < end_of(first_row) ? next + sub : first_row);
       float first[2] = {0.f, 0.f};
       if (!p.rms) {
-        if constexpr (BLOCK || sizeof(T) == 4 || VEC < 4) {  // the means themselves
-          Run<VEC> a0 = n[0][0], a1 = n[1][0];
+        Run<VEC> a0 = n[0][0], a1 = n[1][0];
 #pragma unroll
-          for (int a = 1; a < NV; ++a) {
-            add(a0, a0, n[0][a]);
-            add(a1, a1, n[1][a]);
-          }
-          first[0] = total(a0) * at.inv;
-          first[1] = total(a1) * at.inv;
-          red.sum<BLOCK>(first);
-        } else {  // a row's first lane's
-          const int from = (threadIdx.x & 31) & ~(red.lanes - 1);
-          first[0] = __shfl_sync(0xffffffffu, total(n[0][0]) * (1.f / VEC), from);
-          if constexpr (POST) first[1] = __shfl_sync(0xffffffffu, total(n[1][0]) * (1.f / VEC), from);
+        for (int a = 1; a < NV; ++a) {
+          add(a0, a0, n[0][a]);
+          add(a1, a1, n[1][a]);
         }
+        first[0] = total(a0) * at.inv;
+        first[1] = total(a1) * at.inv;
+        red.sum<BLOCK>(first);
       }
       backward_row<T, BLOCK, POST, ONE>(p, n, t, dx, first, live ? base + sub : seg, live, at, c, red, sums, [] {});
     }
@@ -816,11 +813,15 @@ template <typename T, int VEC> NA_DEVICE void read_shared(Run<VEC>& d, uint32_t 
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(at));
   unpack<T>(d, *reinterpret_cast<const Pack<T, VEC>*>(&u));
 }
-// The mean of the first VEC of a row in shared memory.
+// The mean of the first 8 VEC values of a row in shared memory, which wide rows
+// have, by each warp for itself: no barrier.  Of 32 VEC, 3% slower.
 template <typename T, int VEC> NA_DEVICE float first_of(uint32_t at) {
   Run<VEC> r;
-  read_shared<T>(r, at);
-  return total(r) * (1.f / VEC);
+  read_shared<T>(r, at + (threadIdx.x & 7) * VEC * (uint32_t)sizeof(T));
+  float s = total(r);
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s * (1.f / (8 * VEC));
 }
 NA_DEVICE void ring_init(const Ring& ring, volatile int* abort_flag) {
   if (threadIdx.x == 0) {
