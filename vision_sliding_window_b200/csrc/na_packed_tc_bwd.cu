@@ -47,46 +47,55 @@ template <int D> struct Bwd {
   static constexpr int B_OFF = A_OFF + SA * G::TILE_BYTES;
   static constexpr int TERMS_OFF = B_OFF + SB * G::TILE_BYTES;
   static constexpr int BAR_OFF = TERMS_OFF + ST * 2 * kTile * 4;
-  static constexpr int SMEM = BAR_OFF + 256;
+  static constexpr int kBars = 15 + 2 * SA + 2 * SB + 2 * ST;
+  static constexpr int TMEM_SLOT = kBars * 8, ABORT = TMEM_SLOT + 4;
+  static constexpr int SMEM = BAR_OFF + (ABORT + 4 + 15) / 16 * 16;
   static constexpr int SMEM_ASKED = SMEM > 116 * 1024 ? SMEM : 116 * 1024;  // one block an SM: it holds all of tensor memory
   static_assert(SMEM <= kMaxSmem, "fits");
   static constexpr int THREADS = 384;
   static constexpr int REGS_CTRL = 72, REGS_WORK = 216;
-  static constexpr int kBars = 9 + 2 * SA + 2 * SB + 2 * ST;
-  static_assert(kBars * 8 + 8 <= 256, "fits");
 };
 
 // The barriers, and the two words behind them: tensor memory's address and the
 // block's abort flag.
+//
+// What is done once a step has two barriers, used in turn: step i waits for
+// phase i / 2 of the (i & 1)-th.  With one, a warp held back for a step would
+// find two phases complete, which its parity cannot tell from none, and wait
+// for good: the dq kernel's S is made a step ahead, and a `turn` is announced
+// before the last one needs to have been looked at.  Step i + 2 of each is only
+// begun after all that wait for step i have passed it.
 template <int D> struct Bars {
   using C = Bwd<D>;
   uint32_t base;
   NA_DEVICE uint32_t kept() const { return base; }
   NA_DEVICE uint32_t done() const { return base + 8; }
-  NA_DEVICE uint32_t s() const { return base + 16; }
-  NA_DEVICE uint32_t dp() const { return base + 24; }
-  NA_DEVICE uint32_t p_ready() const { return base + 32; }
-  NA_DEVICE uint32_t ds_ready() const { return base + 40; }
-  NA_DEVICE uint32_t tail() const { return base + 48; }  // of both rings' last tile
-  NA_DEVICE uint32_t p_half() const { return base + 64; }
-  NA_DEVICE uint32_t turn() const { return base + 56; }  // of the other MMA warp
-  NA_DEVICE uint32_t full_a(int i) const { return base + 72 + (i % C::SA) * 8; }
-  NA_DEVICE uint32_t empty_a(int i) const { return base + 72 + (C::SA + i % C::SA) * 8; }
-  NA_DEVICE uint32_t full_b(int i) const { return base + 72 + (2 * C::SA + i % C::SB) * 8; }
-  NA_DEVICE uint32_t empty_b(int i) const { return base + 72 + (2 * C::SA + C::SB + i % C::SB) * 8; }
-  NA_DEVICE uint32_t full_t(int i) const { return base + 72 + (2 * C::SA + 2 * C::SB + i % C::ST) * 8; }
-  NA_DEVICE uint32_t empty_t(int i) const { return base + 72 + (2 * C::SA + 2 * C::SB + C::ST + i % C::ST) * 8; }
-  NA_DEVICE uint32_t tmem_slot() const { return base + 248; }
+  NA_DEVICE uint32_t tail() const { return base + 16; }  // of both rings' last tile
+  NA_DEVICE uint32_t s(int i) const { return base + 24 + (i & 1) * 8; }
+  NA_DEVICE uint32_t dp(int i) const { return base + 40 + (i & 1) * 8; }
+  NA_DEVICE uint32_t p_half(int i) const { return base + 56 + (i & 1) * 8; }
+  NA_DEVICE uint32_t p_ready(int i) const { return base + 72 + (i & 1) * 8; }
+  NA_DEVICE uint32_t ds_ready(int i) const { return base + 88 + (i & 1) * 8; }
+  NA_DEVICE uint32_t turn(int i) const { return base + 104 + (i & 1) * 8; }  // of the other MMA warp
+  NA_DEVICE uint32_t full_a(int i) const { return base + 120 + (i % C::SA) * 8; }
+  NA_DEVICE uint32_t empty_a(int i) const { return base + 120 + (C::SA + i % C::SA) * 8; }
+  NA_DEVICE uint32_t full_b(int i) const { return base + 120 + (2 * C::SA + i % C::SB) * 8; }
+  NA_DEVICE uint32_t empty_b(int i) const { return base + 120 + (2 * C::SA + C::SB + i % C::SB) * 8; }
+  NA_DEVICE uint32_t full_t(int i) const { return base + 120 + (2 * C::SA + 2 * C::SB + i % C::ST) * 8; }
+  NA_DEVICE uint32_t empty_t(int i) const { return base + 120 + (2 * C::SA + 2 * C::SB + C::ST + i % C::ST) * 8; }
+  NA_DEVICE uint32_t tmem_slot() const { return base + C::TMEM_SLOT; }
   NA_DEVICE void init(int empty_b_count) const {
     mbar_init(kept(), 1);
     mbar_init(done(), 2);  // both MMA warps'
-    mbar_init(s(), 1);
-    mbar_init(dp(), 1);
-    mbar_init(p_ready(), 8);
-    mbar_init(p_half(), 8);
-    mbar_init(ds_ready(), 8);
     mbar_init(tail(), 2);
-    mbar_init(turn(), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s(i), 1);
+      mbar_init(dp(i), 1);
+      mbar_init(p_half(i), 8);
+      mbar_init(p_ready(i), 8);
+      mbar_init(ds_ready(i), 8);
+      mbar_init(turn(i), 1);
+    }
     for (int i = 0; i < C::SA; ++i) mbar_init(full_a(i), 1), mbar_init(empty_a(i), 1);
     for (int i = 0; i < C::SB; ++i) mbar_init(full_b(i), 1), mbar_init(empty_b(i), empty_b_count);
     for (int i = 0; i < C::ST; ++i) mbar_init(full_t(i), 1), mbar_init(empty_t(i), 8);
@@ -178,7 +187,7 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
   auto o_tile = [&](int i) { return base + C::B_OFF + (i % C::SB) * G::TILE_BYTES; };
   auto lse_of = [&](int i) { return reinterpret_cast<float*>(raw + C::TERMS_OFF) + (i % C::ST) * 2 * kTile; };
   const Bars<D> bar{base + C::BAR_OFF};
-  volatile int* ab = reinterpret_cast<volatile int*>(raw + C::BAR_OFF + 252);
+  volatile int* ab = reinterpret_cast<volatile int*>(raw + C::BAR_OFF + C::ABORT);
   if (threadIdx.x == 0) {
     *ab = 0;
     bar.init(2);  // dO goes into dP and dV
@@ -189,7 +198,7 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(raw + C::BAR_OFF + 248);
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(raw + C::BAR_OFF + C::TMEM_SLOT);
   const uint32_t s_at = tmem, dp_at = tmem + 128, dv_at = tmem + 256, dk_at = tmem + 256 + D;
   constexpr float kLift = BF16 ? 0.f : 15.f, kUnlift = BF16 ? 1.f : 1.f / 32768.f;
 
@@ -243,7 +252,7 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       const bool first_warp = warp == 1;
       const uint32_t at = first_warp ? s_at : dp_at, to = first_warp ? dv_at : dk_at;
       const uint32_t kept = first_warp ? k_tile : v_tile;
-      const uint32_t ready = first_warp ? bar.p_ready() : bar.ds_ready(), made = first_warp ? bar.s() : bar.dp();
+      auto made = [&](int i) { return first_warp ? bar.s(i) : bar.dp(i); };
       // S^T is made of a row tile's Q and dV summed with its dO; dP^T and dK the other way round
       auto with = [&](int i) { return first_warp ? q_tile(i) : o_tile(i); };
       auto sums = [&](int i) { return first_warp ? o_tile(i) : q_tile(i); };
@@ -254,7 +263,7 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         tc_fence_after();
         if (elect_one()) {
           mma_rows_by_rows<D, BF16>(at, kept, with(0));
-          mma_commit(made);
+          mma_commit(made(0));
           if (!first_warp) mma_commit(bar.empty_b(0));
         }
         for (int i = 0; i < n; ++i) {
@@ -264,7 +273,7 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
           if (i + 1 < n) ok = ok && (first_warp ? wait_a(i + 1) : wait_b(i + 1));
           if (first_warp) {
             // P^T comes in halves: 32 of each warpgroup's 64 columns
-            ok = ok && mbar_wait(bar.p_half(), i & 1, ab, p.status);
+            ok = ok && mbar_wait(bar.p_half(i), (i >> 1) & 1, ab, p.status);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
             if (elect_one()) {
@@ -272,8 +281,8 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
               mma_weights_by_tile<D, BF16, 64, 4, 6>(to, at, sums(i), true);
             }
           }
-          ok = ok && mbar_wait(ready, i & 1, ab, p.status);
-          if (!first_warp) ok = ok && mbar_wait(bar.turn(), i & 1, ab, p.status);
+          ok = ok && mbar_wait(first_warp ? bar.p_ready(i) : bar.ds_ready(i), (i >> 1) & 1, ab, p.status);
+          if (!first_warp) ok = ok && mbar_wait(bar.turn(i), (i >> 1) & 1, ab, p.status);
           if (!__all_sync(0xffffffffu, ok)) break;
           tc_fence_after();
           if (elect_one()) {
@@ -286,10 +295,10 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
             mma_commit(first_warp ? bar.empty_b(i) : bar.empty_a(i));
             if (i + 1 < n) {
               mma_rows_by_rows<D, BF16>(at, kept, with(i + 1));
-              mma_commit(made);
+              mma_commit(made(i + 1));
               if (!first_warp) mma_commit(bar.empty_b(i + 1));
             }
-            if (first_warp) mbar_arrive(bar.turn());
+            if (first_warp) mbar_arrive(bar.turn(i));
           }
         }
       }
@@ -312,7 +321,7 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     bool ok = true;
     for (int i = 0; i < n; ++i) {
       if (!(ok = mbar_wait(bar.full_t(i), (i / C::ST) & 1, ab, p.status))) break;
-      if (!(ok = mbar_wait(bar.s(), i & 1, ab, p.status))) break;
+      if (!(ok = mbar_wait(bar.s(i), (i >> 1) & 1, ab, p.status))) break;
       tc_fence_after();
       const int pos = tile_pos(i);
       const bool masked = pos < all_lo || pos + P > all_hi;
@@ -354,14 +363,14 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(c == 0 ? bar.p_half() : bar.p_ready());
+        if (lane == 0) mbar_arrive(c == 0 ? bar.p_half(i) : bar.p_ready(i));
       }
       };
       if (masked)
         weights(std::false_type{});
       else
         weights(std::true_type{});
-      if (!(ok = mbar_wait(bar.dp(), i & 1, ab, p.status))) break;
+      if (!(ok = mbar_wait(bar.dp(i), (i >> 1) & 1, ab, p.status))) break;
       tc_fence_after();
       uint32_t y[2][32];
       tmem_ld32(my_dp, y[0]);
@@ -391,7 +400,7 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(bar.ds_ready());
+        mbar_arrive(bar.ds_ready(i));
         mbar_arrive(bar.empty_t(i));
       }
     }
@@ -531,7 +540,7 @@ packed_dq_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
   auto k_tile = [&](int i) { return base + C::A_OFF + (i % C::SA) * G::TILE_BYTES; };
   auto v_tile = [&](int i) { return base + C::B_OFF + (i % C::SB) * G::TILE_BYTES; };
   const Bars<D> bar{base + C::BAR_OFF};
-  volatile int* ab = reinterpret_cast<volatile int*>(raw + C::BAR_OFF + 252);
+  volatile int* ab = reinterpret_cast<volatile int*>(raw + C::BAR_OFF + C::ABORT);
   if (threadIdx.x == 0) {
     *ab = 0;
     bar.init(1);
@@ -540,7 +549,7 @@ packed_dq_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(raw + C::BAR_OFF + 248);
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(raw + C::BAR_OFF + C::TMEM_SLOT);
   const uint32_t dp_at = tmem + 256, dq_at = tmem + 384;  // S in two slots of 128 columns
 
   if (warp < 4) {
@@ -577,10 +586,10 @@ packed_dq_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
         if (elect_one()) {
           if (warp == 1) {
             mma_rows_by_rows<D, BF16>(tmem, q_tile, k_tile(0));
-            mma_commit(bar.s());
+            mma_commit(bar.s(0));
           } else {
             mma_rows_by_rows<D, BF16>(dp_at, o_tile, v_tile(0));
-            mma_commit(bar.dp());
+            mma_commit(bar.dp(0));
             mma_commit(bar.empty_b(0));
           }
         }
@@ -590,11 +599,11 @@ packed_dq_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
             tc_fence_after();
             if (elect_one()) {
               mma_rows_by_rows<D, BF16>(tmem + ((i + 1) & 1) * kTile, q_tile, k_tile(i + 1));
-              mma_commit(bar.s());
+              mma_commit(bar.s(i + 1));
             }
           }
-          ok = mbar_wait(bar.ds_ready(), i & 1, ab, p.status);
-          if (warp == 1) ok = ok && mbar_wait(bar.turn(), i & 1, ab, p.status);
+          ok = mbar_wait(bar.ds_ready(i), (i >> 1) & 1, ab, p.status);
+          if (warp == 1) ok = ok && mbar_wait(bar.turn(i), (i >> 1) & 1, ab, p.status);
           if (warp == 2 && i + 1 < n) ok = ok && wait_b(i + 1);
           if (!__all_sync(0xffffffffu, ok)) break;
           tc_fence_after();
@@ -605,10 +614,10 @@ packed_dq_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
             } else {
               if (i + 1 < n) {
                 mma_rows_by_rows<D, BF16>(dp_at, o_tile, v_tile(i + 1));
-                mma_commit(bar.dp());
+                mma_commit(bar.dp(i + 1));
                 mma_commit(bar.empty_b(i + 1));
               }
-              mbar_arrive(bar.turn());
+              mbar_arrive(bar.turn(i));
             }
           }
         }
@@ -635,7 +644,7 @@ packed_dq_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
     auto meet = [] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
     for (int i = 0; i < n; ++i) {
       const uint32_t my_s = tmem + lanes + (i & 1) * kTile + half * 64, my_dp = dp_at + lanes + half * 64;
-      if (!(ok = mbar_wait(bar.s(), i & 1, ab, p.status))) {
+      if (!(ok = mbar_wait(bar.s(i), (i >> 1) & 1, ab, p.status))) {
         if (n == 1) meet();
         break;
       }
@@ -670,7 +679,7 @@ packed_dq_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
         weights(std::false_type{});
       else
         weights(std::true_type{});
-      if (!(ok = mbar_wait(bar.dp(), i & 1, ab, p.status))) {
+      if (!(ok = mbar_wait(bar.dp(i), (i >> 1) & 1, ab, p.status))) {
         if (n == 1) meet();
         break;
       }
@@ -712,7 +721,7 @@ packed_dq_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar.ds_ready());
+      if (lane == 0) mbar_arrive(bar.ds_ready(i));
     }
     if (ok && n > 0) ok = mbar_wait(bar.done(), 0, ab, p.status);
     if (ok) {
