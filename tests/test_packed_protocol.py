@@ -388,3 +388,85 @@ def test_one_barrier_for_all_steps_can_be_overrun(kernel, names, one):
         for n in (3, 5, 9):
             for seed in range(400):
                 kernel(n, seed, 4, 4, False, *(1 if name == one else 2 for name in names))
+
+
+# ------------------------------------------------------------- waits given up
+# A wait that runs out raises the block's flag and every other wait gives up
+# too.  Copies that are in flight then must have landed before the block ends.
+def source_of(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return f.read()
+
+
+def given_up(slots, n, seed, settles):
+    """A warp that loads n tiles into a ring, a warp that uses them, and a wait of
+    either that runs out while the loads that are in flight are late."""
+    rnd = random.Random(seed)
+    full, empty = InTurn("full", slots), InTurn("empty", slots)
+    loads, gave_up, at = [], [False], rnd.randint(0, 3 * n)
+
+    def wait(bar, i):
+        b = bar.slots[i % slots]
+        while (b.done & 1) == ((i // slots) & 1):
+            if gave_up[0]:
+                return False
+            yield
+        return True
+
+    def loader():
+        asked = 0
+        for i in range(n):
+            if i >= slots and not (yield from wait(empty, i - slots)):
+                break
+            loads.append(i)
+            asked += 1
+            yield
+        if settles:
+            for u in range(max(0, asked - slots), asked):
+                while u in loads:
+                    yield
+
+    def user():
+        for i in range(n):
+            if not (yield from wait(full, i)):
+                break
+            empty.arrive(i)
+            yield
+
+    roles, late = [loader(), user()], rnd.random()
+    for step in range(10000):
+        if step >= at:
+            gave_up[0] = True
+        if loads and rnd.random() > late:
+            i = loads.pop(rnd.randrange(len(loads)))
+            full.arrive(i)
+        if roles:
+            r = rnd.choice(roles)
+            if next(r, "over") == "over":
+                roles.remove(r)
+        if not roles:
+            if loads:
+                raise Stuck(f"tiles {loads} in flight when the block ended")
+            return
+    raise Stuck("deadlock")
+
+
+@pytest.mark.parametrize("kernel", ["na_packed_tc.cu", "na_packed_tc_bwd.cu", "na_packed_rows.cu", "na_norm.cu"])
+def test_no_copy_is_in_flight_when_a_block_ends(kernel):
+    source = source_of(kernel)
+    if kernel == "na_norm.cu":  # the warp that asks settles before it leaves
+        left = re.findall(r"if \(!__all_sync\(0xffffffffu, mbar_wait\([^;{]*\{\n\s*if \(threadIdx.x < 32\) ring_settle\(", source)
+        settles = len(left) == source.count("mbar_wait(ring.bar(it)") == 2
+    else:  # every loading warp settles, whether or not a wait was given up by then
+        loops = len(re.findall(r"-- loads|- loads: ", source))
+        settles = len(re.findall(r"\n      settle_ring\(", source)) == loops > 0
+    for slots in (1, 2, 4, 8):
+        for n in (1, 3, 9, 20):
+            for seed in range(100):
+                given_up(slots, n, seed, settles)
+
+
+def test_a_loading_warp_that_leaves_at_once_is_found():
+    with pytest.raises(Stuck, match="in flight"):
+        for seed in range(100):
+            given_up(4, 9, seed, False)

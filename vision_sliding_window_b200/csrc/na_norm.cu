@@ -804,8 +804,8 @@ constexpr int kMaxStages = 8;
 struct Ring {
   uint32_t data, bars, stage_bytes, row_bytes;
   int stages;
-  NA_DEVICE uint32_t at(long long it) const { return data + (uint32_t)(it % stages) * stage_bytes; }
-  NA_DEVICE uint32_t bar(long long it) const { return bars + (uint32_t)(it % stages) * 8; }
+  NA_DEVICE uint32_t at(int it) const { return data + (uint32_t)(it % stages) * stage_bytes; }
+  NA_DEVICE uint32_t bar(int it) const { return bars + (uint32_t)(it % stages) * 8; }
 };
 
 template <typename T, int VEC> NA_DEVICE void read_shared(Run<VEC>& d, uint32_t at) {
@@ -832,6 +832,21 @@ NA_DEVICE void ring_init(const Ring& ring, volatile int* abort_flag) {
   __syncthreads();
 }
 
+// Warps that give up waiting for row `it` leave, each as a whole, so that the
+// barriers of the others keep whole warps.  The one that asks for the rows first
+// lets those land that may be on their way: a copy that came later would write
+// another block's memory.  The limit is for all of them, as those past the
+// block's last row were not asked for.  Kept out of the loop over rows: as part
+// of it, it cost registers that the loop needs (139 us where this takes 104, at
+// 16387 rows of 4096).  Rows are counted in 32 bits: 64 cost 5 us there, in
+// divisions by the number of stages.
+__device__ __noinline__ void ring_settle(uint32_t bars, int it, int stages) {
+  const unsigned long long t0 = globaltimer_ns();
+  for (int u = it; u < it + stages; ++u)
+    while (!sm100::mbar_try_wait(bars + (uint32_t)(u % stages) * 8, (uint32_t)(u / stages) & 1))
+      if (globaltimer_ns() - t0 > kWaitLimitNs) return;
+}
+
 // Blocks of 256 threads an SM: with weights held (16 bits) registers leave room
 // for two; a third spills, and costs 112 us where two take 106 (16387 rows of
 // 4096).  float32 reads its weights again and has three, 108 us for 143 (8000
@@ -851,8 +866,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? kWideBlocks<T> : 1)
   const bool two = p.o != nullptr;
   const uint32_t row_bytes = (uint32_t)p.C * sizeof(T);
   const Ring ring{smem_addr(ring_data), smem_addr(ring_bars), row_bytes * (two ? 2 : 1), row_bytes, stages};
-  auto ask = [&](long long it) {  // by thread 0
-    const long long row = blockIdx.x + it * gridDim.x;
+  auto ask = [&](int it) {  // by thread 0
+    const long long row = blockIdx.x + (long long)it * gridDim.x;
     if (row >= p.rows) return;
     mbar_expect_tx(ring.bar(it), ring.stage_bytes);
     bulk_load(ring.at(it), (const T*)p.x + row * p.C, row_bytes, ring.bar(it));
@@ -863,9 +878,12 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? kWideBlocks<T> : 1)
     for (int i = 0; i < stages; ++i) ask(i);
   const Place<NV> at = place_of<VEC, NV, FULL>(threadIdx.x, blockDim.x, p.C);
   ForwardVectors<T, VEC, NV, hold<T, VEC, NV, 16>()> c(p, at);
-  long long it = 0;
+  int it = 0;
   for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, ++it) {
-    if (!mbar_wait(ring.bar(it), (uint32_t)(it / stages) & 1, &abort_flag, p.status)) return;
+    if (!__all_sync(0xffffffffu, mbar_wait(ring.bar(it), (uint32_t)(it / stages) & 1, &abort_flag, p.status))) {
+      if (threadIdx.x < 32) ring_settle(ring.bars, it, stages);
+      return;
+    }
     Run<VEC> y[NV], v[NV];
     NA_RUNS(a) {
       set(y[a], 0.f);
@@ -897,7 +915,7 @@ __global__ void __launch_bounds__(512, 1) norm_backward_wide_kernel(NormArgs p, 
   const Ring ring{smem_addr(ring_data), smem_addr(ring_bars), o_off + (has_o ? row_bytes : 0), row_bytes, stages};
   long long r0, r1;
   chunk_rows_of(p, blockIdx.x, &r0, &r1);
-  auto ask = [&](long long it) {  // by thread 0
+  auto ask = [&](int it) {  // by thread 0
     const long long row = r0 + it;
     if (row >= r1) return;
     const uint32_t to = ring.at(it), bar = ring.bar(it);
@@ -917,9 +935,12 @@ __global__ void __launch_bounds__(512, 1) norm_backward_wide_kernel(NormArgs p, 
   Sums<NV, VEC> sums;
   long long gate_row = r0 < r1 ? gate_of(p, r0) : 0, gate_end = (gate_row + 1) * p.gate_rows;
   c.at_gate(p, at, gate_row);
-  long long it = 0;
+  int it = 0;
   for (long long row = r0; row < r1; ++row, ++it) {
-    if (!mbar_wait(ring.bar(it), (uint32_t)(it / stages) & 1, &abort_flag, p.status)) return;
+    if (!__all_sync(0xffffffffu, mbar_wait(ring.bar(it), (uint32_t)(it / stages) & 1, &abort_flag, p.status))) {
+      if (threadIdx.x < 32) ring_settle(ring.bars, it, stages);
+      return;
+    }
     Run<VEC> n[2][NV], t[NV], dx[NV];
     NA_RUNS(a) {
       set(n[0][a], 0.f);

@@ -161,6 +161,9 @@ packed_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
   const T* vbase = (const T*)p.v + ((long long)sp.k0 * p.hk + kh) * D;
   int done = 0;  // tiles of earlier row tiles, which went through the ring too
   for (long long r0 = 0; r0 < all_rows; r0 += 16) {
+    // After a wait was given up the ring's barriers mean nothing.  The block
+    // still walks the rows, without tiles: its cluster meets at every one.
+    const bool gave_up = abort_flag;
     const int n = (int)min(16ll, all_rows - r0);
     int kb, ke, unused;
     visible(p, sp, (int)(r0 / p.group), &kb, &unused);
@@ -173,10 +176,11 @@ packed_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
       ke = min(ke, kb + (int)((long long)tiles * (rank + 1) / kCluster) * kTileKeys);
       kb = from;
     }
-    const int tiles = ke > kb ? (ke - kb + kTileKeys - 1) / kTileKeys : 0;
+    const int tiles = ke > kb && !gave_up ? (ke - kb + kTileKeys - 1) / kTileKeys : 0;
     if (warp == kWarps) {
       // --------------------------------------------------------------- loads
-      for (int i = 0; i < tiles; ++i) {
+      int i = 0;
+      for (; i < tiles; ++i) {
         const int u = done + i;
         if (u >= R::STAGES && !mbar_wait(empty(u), ((u / R::STAGES) - 1) & 1, &abort_flag, p.status)) break;
         if (lane == 0) {
@@ -190,6 +194,7 @@ packed_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
         }
         __syncwarp();
       }
+      settle_ring(done, i, R::STAGES, full);
     } else {
       // this thread's rows g and g + 8: where they lie and what they see
       int lo[2], hi[2];

@@ -160,7 +160,6 @@ packed_forward_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_co
         mbar_expect_tx(bar_q(), (uint32_t)(TILES * P * p.group * D * 2));
         for (int t = 0; t < TILES; ++t) load_row_tile<D>(q_tile(t), &mq, bar_q(), kh, sp.q0 + pos0 + t * P);
       }
-      bool tail_used = false;
       int i = 0;
       for (; i < 2 * n; ++i) {
         if (i >= SLOTS && !mbar_wait(bar_empty(i), ((i / SLOTS) - 1) & 1, ab, p.status)) break;
@@ -176,18 +175,17 @@ packed_forward_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_co
         }
         __syncwarp();
         if (tail) {
-          tail_used = true;
-          if (!mbar_wait(bar_tail, 0, ab, p.status)) break;
+          if (!mbar_wait(bar_tail, 0, ab, p.status)) {
+            mbar_wait_settle(bar_tail, 0);
+            break;
+          }
           zero_rows<D>(slot(i), sp.nk - k0);
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_full(i));
         }
       }
-      if (*ab) {  // leave no copy in flight
-        mbar_wait_settle(bar_q(), 0);
-        if (tail_used) mbar_wait_settle(bar_tail, 0);
-        for (int u = max(0, i - SLOTS); u < i; ++u) mbar_wait_settle(bar_full(u), (u / SLOTS) & 1);
-      }
+      mbar_wait_settle(bar_q(), 0);
+      settle_ring(0, i, SLOTS, bar_full);
     } else if (warp == 1 && n > 0) {
       // ----------------------------------------------------------- S = Q K^T
       // The whole warp walks the steps, which keeps what the operands are made

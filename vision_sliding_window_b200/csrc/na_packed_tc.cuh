@@ -129,11 +129,22 @@ NA_DEVICE bool load_ring_tile(uint32_t slot, uint32_t full, uint32_t tail, int l
   }
   __syncwarp();
   if (!cut) return true;
-  if (!mbar_wait(tail, 0, ab, status)) return false;
+  if (!mbar_wait(tail, 0, ab, status)) {
+    mbar_wait_settle(tail, 0);
+    return false;
+  }
   zero_rows<D>(slot, left);
   __syncwarp();
   if (lane == 0) mbar_arrive(full);
   return true;
+}
+
+// The last thing a loading warp does: of the tiles that it asked for, `count`
+// from the `first` on, the last `slots` may still be on their way, also where a
+// wait was given up.  A copy that landed after its block has ended would write
+// another block's memory.
+template <typename F> NA_DEVICE void settle_ring(int first, int count, int slots, F full) {
+  for (int u = first + max(0, count - slots); u < first + count; ++u) mbar_wait_settle(full(u), (u / slots) & 1);
 }
 
 // 2^x without the special-function unit, which bounds a softmax fed by the

@@ -235,13 +235,14 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         const uint32_t empty = first_warp ? bar.empty_a(i) : bar.empty_b(i);
         const int slots = first_warp ? C::SA : C::SB;
         if (i >= slots && !mbar_wait(empty, ((i / slots) - 1) & 1, ab, p.status)) break;
-        load_ring_tile<D>(first_warp ? q_tile(i) : o_tile(i), first_warp ? bar.full_a(i) : bar.full_b(i), bar.tail(),
+        if (!load_ring_tile<D>(first_warp ? q_tile(i) : o_tile(i), first_warp ? bar.full_a(i) : bar.full_b(i), bar.tail(),
                           (sp.nq - pos) * p.group, P * p.group, bytes, ab, p.status, [&](uint32_t dst, uint32_t b) {
                             load_row_tile<D>(dst, first_warp ? &mq : &mo, b, kh, sp.q0 + pos);
-                          });
+                          }))
+          break;
       }
-      if (*ab && first_warp) mbar_wait_settle(bar.kept(), 0);
-      if (*ab) mbar_wait_settle(first_warp ? bar.full_a(max(i, 1) - 1) : bar.full_b(max(i, 1) - 1), 0);
+      if (first_warp) mbar_wait_settle(bar.kept(), 0);
+      settle_ring(0, i, first_warp ? C::SA : C::SB, [&](int u) { return first_warp ? bar.full_a(u) : bar.full_b(u); });
     } else if ((warp == 1 || warp == 3) && n > 0) {
       // -------------------------------------------------------------- MMAs
       // One warp for S^T and dV, one for dP^T and dK: each runs its two in
@@ -567,13 +568,14 @@ packed_dq_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
         const int k0 = kb + i * kTile, slots = first_warp ? C::SA : C::SB;
         const uint32_t empty = first_warp ? bar.empty_a(i) : bar.empty_b(i);
         if (i >= slots && !mbar_wait(empty, ((i / slots) - 1) & 1, ab, p.status)) break;
-        load_ring_tile<D>(first_warp ? k_tile(i) : v_tile(i), first_warp ? bar.full_a(i) : bar.full_b(i), bar.tail(),
+        if (!load_ring_tile<D>(first_warp ? k_tile(i) : v_tile(i), first_warp ? bar.full_a(i) : bar.full_b(i), bar.tail(),
                           sp.nk - k0, kTile, G::TILE_BYTES, ab, p.status, [&](uint32_t dst, uint32_t b) {
                             load_key_tile<D>(dst, first_warp ? &mk : &mv, b, kh, sp.k0 + k0);
-                          });
+                          }))
+          break;
       }
-      if (*ab && first_warp) mbar_wait_settle(bar.kept(), 0);
-      if (*ab) mbar_wait_settle(first_warp ? bar.full_a(max(i, 1) - 1) : bar.full_b(max(i, 1) - 1), 0);
+      if (first_warp) mbar_wait_settle(bar.kept(), 0);
+      settle_ring(0, i, first_warp ? C::SA : C::SB, [&](int u) { return first_warp ? bar.full_a(u) : bar.full_b(u); });
     } else if ((warp == 1 || warp == 2) && n > 0) {
       // -------------------------------------------------------------- MMAs
       // One warp for S and dQ, one for dP, for the same reason as above; dQ waits
