@@ -161,11 +161,12 @@ template <typename T, int D> NA_DEVICE float dot_row(const T* a, const T* b) {
 // One row over its keys [lo, hi) by a whole warp, from global memory: every
 // key outside is left out of the sums, not multiplied by zero.  Matrix
 // instructions cannot leave out single entries, so a row whose result is not
-// finite is taken again by this.  acc holds the columns lane + 32 e, not yet
-// divided by *sum; logits are in units of log2 with *top as their reference.
+// finite is taken again by this.  acc holds the result's columns lane + 32 e,
+// zeros with an lse of -inf for a row without weights: one that sees no key comes
+// here too, when a value that its neighbours see is not finite.
 template <typename T, int D>
 NA_DEVICE void exact_row(const PackedArgs& p, const T* q, const T* k, const T* v, long long stride, int lo, int hi,
-                         float (&acc)[(D + 31) / 32], float* sum, float* top) {
+                         float (&acc)[(D + 31) / 32], float* lse) {
   const int lane = threadIdx.x & 31;
   const float sl2 = p.scale * kLog2e;
   float m = -INFINITY, l = 0.f;
@@ -189,8 +190,9 @@ NA_DEVICE void exact_row(const PackedArgs& p, const T* q, const T* k, const T* v
         if (lane + 32 * c < D) acc[c] = fmaf(w, to_f<T>(v[(j0 + t) * stride + lane + 32 * c]), acc[c]);
     }
   }
-  *sum = l;
-  *top = m == -INFINITY ? 0.f : m;
+#pragma unroll
+  for (int c = 0; c < (D + 31) / 32; ++c) acc[c] = l == 0.f ? 0.f : acc[c] / l;
+  *lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 }  // namespace packed

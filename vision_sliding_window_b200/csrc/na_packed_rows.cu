@@ -386,10 +386,7 @@ packed_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
         if (__any_sync(0xffffffffu, !finite)) {
           int a, b;
           visible(p, sp, pos, &a, &b);
-          exact_row<T, D>(p, (const T*)p.q + row * D, kbase, vbase, stride, max(a, piece0), min(b, piece1), acc, &l, &m);
-#pragma unroll
-          for (int e = 0; e < (D + 31) / 32; ++e) acc[e] /= l;
-          lse = (m + log2f(l)) * kLn2;
+          exact_row<T, D>(p, (const T*)p.q + row * D, kbase, vbase, stride, max(a, piece0), min(b, piece1), acc, &lse);
         }
         const long long at = CLUSTER ? row : (idx * p.total_q + i) * p.hq + head;
 #pragma unroll

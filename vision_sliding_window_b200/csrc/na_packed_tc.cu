@@ -416,20 +416,18 @@ packed_forward_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_co
         const long long to = __shfl_sync(0xffffffffu, out_row, src), pto = __shfl_sync(0xffffffffu, part_row, src);
         const int l0 = __shfl_sync(0xffffffffu, lo, src), h0 = __shfl_sync(0xffffffffu, hi, src);
         const long long stride = (long long)p.hk * D, first = ((long long)sp.k0 * p.hk + kh) * D;
-        float acc[(D + 31) / 32], l, m;
+        float acc[(D + 31) / 32], again_lse;
         exact_row<T, D>(p, (const T*)p.q + to * D, (const T*)p.k + first, (const T*)p.v + first, stride, l0, h0, acc,
-                        &l, &m);
+                        &again_lse);
 #pragma unroll
         for (int e = 0; e < (D + 31) / 32; ++e) {
           if (lane + 32 * e >= D) continue;
-          const float r = acc[e] / l;
           if (split)
-            p.part_o[pto * D + lane + 32 * e] = r;
+            p.part_o[pto * D + lane + 32 * e] = acc[e];
           else
-            ((T*)p.out)[to * D + lane + 32 * e] = from_f<T>(r);
+            ((T*)p.out)[to * D + lane + 32 * e] = from_f<T>(acc[e]);
         }
         if (lane == 0) {
-          const float again_lse = (m + log2f(l)) * kLn2;
           if (split)
             p.part_lse[pto] = again_lse;
           else if (p.lse)
