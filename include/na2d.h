@@ -221,7 +221,8 @@ na_status na_forward_nd(const void *q, const void *k, const void *v, const void 
  *   s_ij = scale q_i . k_j,  P = softmax over the keys seen,  out_i = sum_j P_ij v_j,
  *   lse[h][i] = ln sum_j e^(s_ij), float32 [heads_q][total_q] (NULL: not written).
  *
- * A row that sees no key gets zeros and an lse of -inf.  Keys that a row does
+ * A row that sees no key gets zeros and an lse of -inf, and so does one whose
+ * logits are all -inf.  Keys that a row does
  * not see, slots past len_k and other sequences never reach its result,
  * whatever they hold (NaN and infinities too).  Rows of q that belong to no
  * sequence are left as they were in out and lse.  The lengths are read on the

@@ -54,3 +54,45 @@ def test_rows_without_keys_beside_values_that_are_not_finite(lq, lk, hq, hk, d, 
     want, wlse, tol, ltol = plain64.forward(q, k, v, cu_q, cu_k, causal=True)
     plain64.check("out", out[lq[0]:], want[lq[0]:], tol[lq[0]:])
     plain64.check("lse", lse, wlse, ltol)
+
+
+NOTHING = [
+    # lq, lk, hq, hk, d, causal
+    ([200, 30], [300, 150], 4, 2, 64, False),
+    ([300], [300], 2, 2, 128, True),
+    ([150], [2600], 2, 1, 32, False),          # keys cut into pieces
+    ([1, 3], [300, 150], 4, 2, 64, False),     # few rows
+    ([2], [9000], 2, 1, 128, False),
+]
+
+
+@pytest.mark.parametrize("lq,lk,hq,hk,d,causal", NOTHING)
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("value", [1.0, math.inf])
+def test_rows_whose_logits_are_all_minus_infinity(lq, lk, hq, hk, d, causal, dtype, value):
+    """They have no weights, as if they saw no key."""
+    q, k, v, cu_q, cu_k, _ = batch(lq, lk, hq, hk, d, dtype, seed=d)
+    q[..., 0] = 1.0
+    k[:lk[0], :, 0] = -math.inf
+    v[:lk[0]] *= value
+    out, lse = na2d.packed_forward(q, k, v, cu_q, cu_k, causal=causal)
+    synchronized()
+    assert (out[:lq[0]] == 0).all() and (lse[:, :lq[0]] == -math.inf).all()
+    want, wlse, tol, ltol = plain64.forward(q[lq[0]:], k[lk[0]:], v[lk[0]:], cu_q[1:] - lq[0], cu_k[1:] - lk[0],
+                                            causal=causal)
+    plain64.check("out", out[lq[0]:], want, tol)
+    plain64.check("lse", lse[:, lq[0]:], wlse, ltol)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("lq", [1, 150])
+@pytest.mark.parametrize("lk,cut", [(600, 300), (9000, 4500)])
+def test_logits_of_minus_infinity_before_others(dtype, lq, lk, cut):
+    q, k, v, cu_q, cu_k, _ = batch([lq], [lk], 4, 2, 64, dtype, seed=7)
+    q[..., 0] = 1.0
+    k[:cut, :, 0] = -math.inf
+    out, lse = na2d.packed_forward(q, k, v, cu_q, cu_k)
+    synchronized()
+    want, wlse, tol, ltol = plain64.forward(q, k[cut:], v[cut:], cu_q, starts([lk - cut]))
+    plain64.check("out", out, want, tol)
+    plain64.check("lse", lse, wlse, ltol)

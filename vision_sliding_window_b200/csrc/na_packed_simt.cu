@@ -184,11 +184,12 @@ NA_DEVICE void weighted_sum(const float* w, const float* b, int ty, int tx, cons
   }
 }
 
+// acc times f; zeros where f is 0, whatever acc holds
 template <typename T, int D, int R>
 NA_DEVICE void store_cols(T* g, int tx, const float (&acc)[Tile<D>::CPT], float f) {
   constexpr int CPT = Tile<D>::CPT, CV = Tile<D>::CV;
 #pragma unroll
-  for (int c = 0; c < CPT; ++c) g[(c / CV) * 8 * CV + tx * CV + c % CV] = from_f<T>(acc[c] * f);
+  for (int c = 0; c < CPT; ++c) g[(c / CV) * 8 * CV + tx * CV + c % CV] = from_f<T>(f == 0.f ? 0.f : acc[c] * f);
 }
 
 template <int D, int ROWS> constexpr int fwd_smem() {

@@ -366,6 +366,8 @@ packed_forward_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_co
       const int head = kh * p.group + row % p.group;
       const long long out_row = i * p.hq + head;
       const long long part_row = ((long long)blockIdx.y * p.total_q + i) * p.hq + head;
+      // every logit was -inf: no weights, where the polynomial made some of 2^-126
+      if (ref == -INFINITY) sum = 0.f;
       // a row that saw no key: zeros and -inf
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       const float lse = sum == 0.f ? -INFINITY : fmaf(ref, p.scale, (log2f(sum) - kLift) * kLn2);

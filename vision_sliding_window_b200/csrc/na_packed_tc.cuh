@@ -151,8 +151,8 @@ template <typename F> NA_DEVICE void settle_ring(int first, int count, int slots
 // tensor cores: x = n + f with n the nearest integer, 2^f by the polynomial of
 // degree 4 that meets it at the five Chebyshev points of [-1/2, 1/2] (off by at
 // most 4e-6, a hundredth of the rounding of a 16-bit weight), n added to the
-// exponent.  For x < 127; below -126 it gives about 2^-126, and for NaN a number
-// too large for 16 bits.
+// exponent.  For x < 127; below -126 (-inf too) it gives about 2^-126, and for
+// NaN a number too large for 16 bits.
 NA_DEVICE void exp2_poly2(float& a, float& b) {
   constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
   constexpr float c0 = 1.f, c1 = 0.693121016f, c2 = 0.240223497f, c3 = 0.0559219755f, c4 = 0.00966636837f;
