@@ -96,3 +96,21 @@ def test_logits_of_minus_infinity_before_others(dtype, lq, lk, cut):
     want, wlse, tol, ltol = plain64.forward(q, k[cut:], v[cut:], cu_q, starts([lk - cut]))
     plain64.check("out", out, want, tol)
     plain64.check("lse", lse, wlse, ltol)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("lq", [1, 150])
+@pytest.mark.parametrize("lk", [600, 9000])
+def test_a_value_that_is_seen_counts_however_small_its_weight(dtype, lq, lk):
+    """0 * NaN: the first keys' weights vanish beside the later ones', wherever a
+    tile, a warp's share or a piece ends."""
+    q, k, v, cu_q, cu_k, _ = batch([lq], [lk], 2, 1, 64, dtype, seed=8)
+    q[..., 0], k[..., 0] = 16.0, 0.0
+    for cut in (1, 64, 200, 500):
+        k[:cut, :, 0] = -300.0
+        v[:cut] = 0.0
+        v[0, :, 3] = math.nan
+        out, lse = na2d.packed_forward(q, k, v, cu_q, cu_k)
+        synchronized()
+        assert torch.isnan(out[..., 3]).all() and torch.isfinite(out[..., :3].float()).all()
+        assert torch.isfinite(lse).all()

@@ -266,7 +266,7 @@ packed_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
 #pragma unroll
             for (int i = 0; i < R::VE; ++i)
 #pragma unroll
-              for (int x = 0; x < 4; ++x) o[c][i][x] = f[x >> 1] == 0.f ? 0.f : o[c][i][x] * f[x >> 1];
+              for (int x = 0; x < 4; ++x) o[c][i][x] *= f[x >> 1];  // NaN stays, also under 0
         }
         uint32_t pa[4];
 #pragma unroll
@@ -338,7 +338,7 @@ packed_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
           float acc = 0.f;
 #pragma unroll
           for (int w = 0; w < kWarps; ++w)
-            if (f[w] != 0.f) acc = fmaf(so[(w * 16 + r) * R::LD + lane + 32 * e], f[w], acc);
+            acc = fmaf(so[(w * 16 + r) * R::LD + lane + 32 * e], f[w], acc);
           so[r * R::LD + lane + 32 * e] = acc;
         }
         if (lane == 0) jm[r] = m, jl[r] = l;
@@ -374,7 +374,7 @@ packed_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
             for (int b = 0; b < B; ++b) {
               const float* at = so + r * R::LD + lane + 32 * e;
               const float v = CLUSTER ? ld_cluster(at, b) : *at;
-              if (f[b] != 0.f) acc[e] = fmaf(v, f[b], acc[e]);
+              acc[e] = fmaf(v, f[b], acc[e]);
             }
           acc[e] *= inv;
           finite = finite && fabsf(acc[e]) < INFINITY;

@@ -362,9 +362,9 @@ __global__ void __launch_bounds__(256) packed_join_kernel(PackedArgs p) {
   const float ref = mx == -INFINITY ? 0.f : mx;
   float acc[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
   for (int c = c0; c < c1; ++c) {
-    const float w = expf(p.part_lse[c * step + row] - ref);
+    const float lse = p.part_lse[c * step + row], w = expf(lse - ref);
     sum += w;
-    if (w == 0.f) continue;  // a piece of which the row saw nothing
+    if (lse == -INFINITY) continue;  // a piece of which the row saw nothing
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       if (lane + 32 * e < p.d) acc[e] = fmaf(w, p.part_o[(c * step + row) * p.d + lane + 32 * e], acc[e]);

@@ -311,7 +311,7 @@ packed_forward_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_co
           if constexpr (W == 32) tmem_ld32(o_at + W * c, o); else tmem_ld16(o_at, o);
           tmem_wait_ld_regs(o);
 #pragma unroll
-          for (int i = 0; i < W; ++i) o[i] = f == 0.f ? 0u : __float_as_uint(__uint_as_float(o[i]) * f);
+          for (int i = 0; i < W; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);  // NaN stays, also under 0
           if constexpr (W == 32) tmem_st32(o_at + W * c, o); else tmem_st16(o_at, o);
         }
       }
