@@ -114,3 +114,104 @@ def test_a_value_that_is_seen_counts_however_small_its_weight(dtype, lq, lk):
         synchronized()
         assert torch.isnan(out[..., 3]).all() and torch.isfinite(out[..., :3].float()).all()
         assert torch.isfinite(lse).all()
+
+
+# ------------------------------------------------------------------ gradients
+def bounds_of_gradients(q, k, v, out, lse, dout, cu_q, cu_k, causal, window, scale):
+    """The gradients in 64 bits and their bounds, as plain64.backward, but with the
+    sum over a row that a kernel takes: dout . out, of the out that was given, or,
+    in the tensor-core kernel for a row tile whose keys lie in one tile, sum P dP.
+    float16 weights' gradients are lifted so that dout's row (for dk the largest of
+    the sequence and group) has a norm of 16 to 32: half a subnormal step of theirs
+    is 2^-25 of a sixteenth of that norm at most; weights are lifted by 2^15."""
+    d, hq, group = q.shape[2], q.shape[1], q.shape[1] // k.shape[1]
+    half = q.dtype == torch.float16
+    u = plain64.half_step(q.dtype)
+    tensor_cores = q.dtype != torch.float32 and group <= 128
+    zeros = [torch.zeros(t.shape, dtype=torch.float64, device=q.device) for t in (q, k, v)]
+    bound = [torch.zeros_like(t) for t in zeros]
+    for q0, lq, k0, lk in plain64.spans(cu_q, cu_k, None):
+        if lq == 0 or lk == 0:
+            continue
+        keep = plain64.visible(lq, lk, causal, window, q.device)
+        per = 128 // max(group, 1) if tensor_cores else 1
+        of_weights = torch.zeros(lq, 1, dtype=torch.bool, device=q.device)
+        if tensor_cores:
+            for a in range(0, lq, per):
+                seen = keep[a:a + per].any(0).nonzero()
+                if len(seen) and int(seen[-1]) - int(seen[0]) < 128:
+                    of_weights[a:a + per] = True
+        for h in range(hq):
+            g = h // group
+            a, go = q[q0:q0 + lq, h].double(), dout[q0:q0 + lq, h].double()
+            b, c = k[k0:k0 + lk, g].double(), v[k0:k0 + lk, g].double()
+            s, _, e = plain64._terms(a, b, keep, scale)
+            l = lse[h, q0:q0 + lq].double()
+            p = (s - l.nan_to_num(neginf=0.0)[:, None]).exp()
+            e = e + 4 * F * l.nan_to_num(neginf=0.0).abs()[:, None]
+            dp = go @ c.t()
+            dp_err = (d + 4) * F * (go.abs() @ c.abs().t())
+            o = out[q0:q0 + lq, h].double()
+            delta = torch.where(of_weights, (p * dp).sum(1, keepdim=True), (go * o).sum(1, keepdim=True))
+            delta_err = torch.where(of_weights, (p * (dp_err + (e + lk * F) * dp.abs())).sum(1, keepdim=True),
+                                    (d + 4) * F * (go * o).abs().sum(1, keepdim=True))
+            norm = dout[q0:q0 + lq, g * group:(g + 1) * group].double().norm(dim=-1).amax()
+            sub = 2.0 ** -25 / 16 if half else 0.0
+            ds = p * (dp - delta)
+            ds_err = p * (dp_err + delta_err) + (e + u) * ds.abs()
+            dq_err, dk_err = ds_err + sub * keep * go.norm(dim=1, keepdim=True), ds_err + sub * keep * norm
+            p_err = p * (e + u) + (2.0 ** -40 * keep if half else 0.0)
+            for n, at, value, error in (
+                    (0, (slice(q0, q0 + lq), h), scale * (ds @ b), scale * (dq_err @ b.abs() + lk * F * (ds.abs() @ b.abs()))),
+                    (1, (slice(k0, k0 + lk), g), scale * (ds.t() @ a),
+                     scale * (dk_err.t() @ a.abs() + lq * group * F * (ds.abs().t() @ a.abs()))),
+                    (2, (slice(k0, k0 + lk), g), p.t() @ go,
+                     p_err.t() @ go.abs() + lq * group * F * (p.t() @ go.abs()))):
+                zeros[n][at] += value
+                bound[n][at] += error
+    small = 1e-30 + (2.0 ** -25 if half else 0.0)  # the results' own subnormals
+    bound = [t + u * z.abs() + small for t, z in zip(bound, zeros)]
+    if half:  # what rounds to an infinity has to be one
+        zeros = [torch.where(z.abs() >= 65520, z.sign() * math.inf, z) for z in zeros]
+    return zeros, bound
+
+
+def check_gradients(q, k, v, dout, cu_q, cu_k, causal=False, window=0, scale=None):
+    out, lse = na2d.packed_forward(q, k, v, cu_q, cu_k, causal=causal, window=window, scale=scale)
+    got = na2d.packed_backward(q, k, v, out, lse, dout, cu_q, cu_k, causal=causal, window=window, scale=scale)
+    synchronized()
+    scale = q.shape[2] ** -0.5 if scale is None else scale
+    want, tol = bounds_of_gradients(q, k, v, out, lse, dout, cu_q, cu_k, causal, window, scale)
+    for name, *x in zip(("dq", "dk", "dv"), got, want, tol):
+        plain64.check(name, *x)
+    return got
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("bad", [40, 200])
+def test_what_a_row_does_not_see_does_not_reach_its_gradients(dtype, bad):
+    """A key, a value, a row and its gradient that are not finite, within the
+    sequence; with a window of 16 they reach 16 rows and the keys of those."""
+    lens, window = [300, 50], 16
+    q, k, v, cu_q, cu_k, _ = batch(lens, lens, 4, 2, 64, dtype, seed=31)
+    dout = torch.randn_like(q)
+    kw = dict(causal=True, window=window)
+    out, lse = na2d.packed_forward(q, k, v, cu_q, cu_k, **kw)
+    want, tol = bounds_of_gradients(q, k, v, out, lse, dout, cu_q, cu_k, True, window, 0.125)
+    k[bad], v[bad] = math.nan, math.inf
+    q[bad + 60], dout[bad + 60] = math.nan, math.inf
+    out, lse = na2d.packed_forward(q, k, v, cu_q, cu_k, **kw)
+    got = na2d.packed_backward(q, k, v, out, lse, dout, cu_q, cu_k, **kw)
+    synchronized()
+    rows = torch.ones(len(q), dtype=torch.bool, device="cuda")
+    rows[bad:bad + window] = False
+    rows[bad + 60] = False
+    keys = torch.ones(len(k), dtype=torch.bool, device="cuda")
+    for r in (~rows).nonzero().flatten().tolist():
+        keys[r - window + 1:r + 1] = False
+    for name, g, w, t, clean in zip(("dq", "dk", "dv"), got, want, tol, (rows, keys, keys)):
+        plain64.check(name, g[clean], w[clean], t[clean])
+        assert not torch.isfinite(g[~clean].float()).all(-1).any() or name == "dv"
+    again = na2d.packed_backward(q, k, v, out, lse, dout, cu_q, cu_k, **kw)
+    for a, b, clean in zip(got, again, (rows, keys, keys)):
+        assert torch.equal(a[clean], b[clean])

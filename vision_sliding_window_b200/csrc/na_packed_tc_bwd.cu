@@ -140,10 +140,10 @@ template <int W> NA_DEVICE void store_run(float* to, const float (&f)[W]) {
   for (int e = 0; e < W; e += 4) *reinterpret_cast<float4*>(to + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
 }
 
-// The weight and its gradient of one row and key, from global memory.
+// The weight and its gradient of one row and key, from global memory; term holds
+// the row's log-sum-exp and delta, which the dq kernel writes while it runs.
 template <typename T, int D>
-NA_DEVICE void exact_pair(const PackedArgs& p, long long row, long long key, float* w, float* ds) {
-  const float2 term = p.terms[row];
+NA_DEVICE void exact_pair(const PackedArgs& p, float2 term, long long row, long long key, float* w, float* ds) {
   const float s = dot_row<T, D>((const T*)p.q + row * D, (const T*)p.k + key * D);
   const float dp = dot_row<T, D>((const T*)p.dout + row * D, (const T*)p.v + key * D);
   *w = exp2f(fmaf(s, p.scale * kLog2e, -term.x));
@@ -448,7 +448,7 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
             float wgt = 0.f, ds = 0.f;
             const long long mine = min(r + lane, r1 - 1);
             const long long row = ((long long)sp.q0 + mine / p.group) * p.hq + kh * p.group + mine % p.group;
-            if (r + lane < r1) exact_pair<T, D>(p, row, kat / D, &wgt, &ds);
+            if (r + lane < r1) exact_pair<T, D>(p, p.terms[row], row, kat / D, &wgt, &ds);
             for (int t = 0; t < (int)min(32ll, r1 - r); ++t) {
               const float u = __shfl_sync(0xffffffffu, half ? ds : wgt, t);
               const long long rt = __shfl_sync(0xffffffffu, row, t);
@@ -751,10 +751,11 @@ packed_dq_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
         again &= again - 1;
         const int l0 = __shfl_sync(0xffffffffu, lo, src), h0 = __shfl_sync(0xffffffffu, hi, src);
         const long long r = __shfl_sync(0xffffffffu, out_row, src);
+        const float2 t0 = make_float2(__shfl_sync(0xffffffffu, term.x, src), __shfl_sync(0xffffffffu, term.y, src));
         float acc[(D + 31) / 32] = {};
         for (int j = l0; j < h0; j += 32) {
           float wgt, ds = 0.f;
-          if (j + lane < h0) exact_pair<T, D>(p, r, (long long)(sp.k0 + j + lane) * p.hk + kh, &wgt, &ds);
+          if (j + lane < h0) exact_pair<T, D>(p, t0, r, (long long)(sp.k0 + j + lane) * p.hk + kh, &wgt, &ds);
           for (int t = 0; t < min(32, h0 - j); ++t) {
             const float u = __shfl_sync(0xffffffffu, ds, t);
             const T* key = (const T*)p.k + ((long long)(sp.k0 + j + t) * p.hk + kh) * D;
