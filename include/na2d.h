@@ -255,7 +255,9 @@ na_status na_packed_forward(const void *q, const void *k, const void *v, const i
  * out's rounding).  Arguments as the
  * forward's; every key slot belongs to the sequence (there is no len_k).
  * dq, dk and dv are written, not added to; rows of no sequence are left as
- * they were.  Each gradient is summed in a fixed order, so a call's results
+ * they were.  16-bit types round P and dS to dt for their products; fp16 ones
+ * are lifted by powers of two first (dS by dout's norm), so that small ones keep
+ * their bits.  Each gradient is summed in a fixed order, so a call's results
  * do not vary from run to run.  workspace: 256-byte aligned, at least
  * na_packed_backward_workspace_bytes() bytes.
  */

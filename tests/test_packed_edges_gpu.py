@@ -187,6 +187,32 @@ def check_gradients(q, k, v, dout, cu_q, cu_k, causal=False, window=0, scale=Non
     return got
 
 
+@pytest.mark.parametrize("size", [1e-3, 1e-4, 2e-6, 3e3])
+@pytest.mark.parametrize("qstd", [0.125, 8.0])
+@pytest.mark.parametrize("causal", [False, True])
+def test_small_and_large_float16_gradients(size, qstd, causal):
+    """Weights of 1/2300 and gradients far below 1: their product is far below
+    float16's normal numbers.  k's (q's) size brings dq (dk) back among them."""
+    lens = [2300, 70]
+    q, k, v, cu_q, cu_k, _ = batch(lens, lens, 2, 1, 64, "f16", seed=21)
+    dout = batch(lens, lens, 2, 1, 64, "f32", seed=22)[0]
+    if size < 1:
+        dout[2300:] *= 1e-2  # a sequence of its own size
+    dout[::3] *= 1e-3 if size > 1 else 1.0  # rows of theirs
+    check_gradients((q * qstd), (k / qstd), v, (dout * size).half(), cu_q, cu_k, causal)
+
+
+def test_float16_gradients_of_rows_of_zeros_and_of_all_sizes():
+    lens = [300, 129]
+    q, k, v, cu_q, cu_k, _ = batch(lens, lens, 4, 2, 64, "f16", seed=23)
+    dout = batch(lens, lens, 4, 2, 64, "f32", seed=24)[0]
+    dout *= (10.0 ** torch.linspace(-7, 1, len(q), device="cuda"))[:, None, None]
+    dout[5::7] = 0.0
+    check_gradients(q, k, v, dout.half(), cu_q, cu_k)
+    grads = check_gradients(q, k, v, torch.zeros_like(q), cu_q, cu_k, causal=True)
+    assert all((g == 0).all() for g in grads)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("bad", [40, 200])
 def test_what_a_row_does_not_see_does_not_reach_its_gradients(dtype, bad):

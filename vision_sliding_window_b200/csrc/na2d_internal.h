@@ -92,6 +92,10 @@ struct PackedArgs {
   float *part_o, *part_lse;  // [max_pieces][total_q][hq][d] and [max_pieces][total_q][hq];
                              // backward: [max_pieces][2][total_k][hk][d], dv and dk
   float2* terms;  // backward: (lse log2 e, out . dout) of every row, [total_q][hq]
+  // fp16 backward on the tensor cores: the powers of two that lift a row's
+  // weights' gradients into the type's range, [total_q][hq] and, for dk, of a
+  // sequence and key head, [nseq][hk]
+  float *row_lifts, *lifts;
   unsigned* status;
 };
 // Row tiles of 128 that a block of the tensor-core forward owns.

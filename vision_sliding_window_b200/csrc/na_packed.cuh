@@ -114,6 +114,16 @@ NA_DEVICE void find_part_warp(const int* cu, int nseq, int total, int mul, int p
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// What brings an fp16 gradient row of squared norm n2 to a norm of 16 to 32, a
+// power of two.  Rows of zeros and such as are not finite, for which any will do,
+// get the largest there is, that of one entry of 2^-24.
+constexpr float kMostLift = 268435456.f;  // 2^28
+NA_DEVICE float lift_of(float n2) {
+  if (!(n2 > 0.f && n2 < INFINITY)) return kMostLift;
+  const int e = (int)(__float_as_uint(n2) >> 23) - 127;  // 2^e <= n2 < 2^(e + 1)
+  return __uint_as_float((uint32_t)(127 + 4 - (e >> 1)) << 23);
+}
+
 template <typename T> NA_DEVICE float to_f(T x);
 template <> NA_DEVICE float to_f<float>(float x) { return x; }
 template <> NA_DEVICE float to_f<__half>(__half x) { return __half2float(x); }

@@ -377,26 +377,56 @@ __global__ void __launch_bounds__(256) packed_join_kernel(PackedArgs p) {
 }
 
 // ---------------------------------------------------------------- backward
-// Every row's log-sum-exp in units of log2 and delta = out . dout.
+// Every row's log-sum-exp in units of log2 and delta = out . dout, and where
+// asked for its lift.
 template <typename T, int D> __global__ void __launch_bounds__(256) packed_terms_kernel(PackedArgs p) {
   constexpr int VEC = 16 / sizeof(T), LPR = D / VEC;  // lanes a row
   const long long row = ((long long)blockIdx.x * 256 + threadIdx.x) / LPR;
   const int v = threadIdx.x % LPR;
   const bool live = row < (long long)p.total_q * p.hq;
-  float s = 0.f;
+  float s = 0.f, n2 = 0.f;
   if (live) {
     const uint4 a = __ldg(reinterpret_cast<const uint4*>(p.o) + row * LPR + v);
     const uint4 b = __ldg(reinterpret_cast<const uint4*>(p.dout) + row * LPR + v);
     const T *x = reinterpret_cast<const T*>(&a), *y = reinterpret_cast<const T*>(&b);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) s = fmaf(to_f<T>(x[i]), to_f<T>(y[i]), s);
+    if (p.row_lifts)
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) n2 = fmaf(to_f<T>(y[i]), to_f<T>(y[i]), n2);
   }
 #pragma unroll
   for (int o = 1; o < LPR; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (p.row_lifts) {
+#pragma unroll
+    for (int o = 1; o < LPR; o <<= 1) n2 += __shfl_xor_sync(0xffffffffu, n2, o);
+    if (live && v == 0) p.row_lifts[row] = lift_of(n2);
+  }
   if (live && v == 0) {
     const float lse = p.lse_in[row % p.hq * p.total_q + row / p.hq];
     // a row that sees no key has no weights, whatever its gradient holds
     p.terms[row] = lse == -INFINITY ? make_float2(INFINITY, 0.f) : make_float2(lse * kLog2e, s);
+  }
+}
+
+// The lift of a sequence's rows of one key head: that of its largest row.
+__global__ void __launch_bounds__(256) packed_lifts_kernel(PackedArgs p) {
+  __shared__ float least[8];
+  for (long long u = blockIdx.x; u < (long long)p.nseq * p.hk; u += gridDim.x) {
+    const Span sp = span_of(p, (int)(u / p.hk));
+    const int kh = (int)(u % p.hk);
+    float f = kMostLift;
+    for (long long r = threadIdx.x; r < (long long)sp.nq * p.group; r += 256)
+      f = fminf(f, p.row_lifts[(sp.q0 + r / p.group) * p.hq + kh * p.group + r % p.group]);
+    f = -warp_max(-f);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) least[threadIdx.x >> 5] = f;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+      for (int w = 1; w < 8; ++w) f = fminf(f, least[w]);
+      p.lifts[u] = f;
+    }
   }
 }
 
@@ -751,11 +781,23 @@ void packed_backward_plan(PackedArgs* p, na_dtype dt) {
   if (pieces > 1) p->max_pieces = (int)pieces;
 }
 
+// Where the parts of the backward's workspace lie, and its size.
+struct BackwardParts {
+  size_t sums, row_lifts, lifts, size;
+};
+static BackwardParts backward_parts(const PackedArgs& p, na_dtype dt) {  // p as planned
+  BackwardParts w;
+  const bool lifted = p.path == kPathTc && dt == NA_F16;
+  w.sums = up256((size_t)p.total_q * p.hq * 8);
+  w.row_lifts = w.sums + (p.max_pieces > 1 ? up256((size_t)p.max_pieces * p.total_k * p.hk * p.d * 8) : 0);
+  w.lifts = w.row_lifts + (lifted ? up256((size_t)p.total_q * p.hq * 4) : 0);
+  w.size = w.lifts + (lifted ? up256((size_t)p.nseq * p.hk * 4) : 0);
+  return w;
+}
 size_t packed_backward_workspace_bytes(const PackedArgs& p, na_dtype dt) {
   PackedArgs c = p;
   packed_backward_plan(&c, dt);
-  const size_t sums = c.max_pieces > 1 ? (size_t)c.max_pieces * c.total_k * c.hk * c.d * 8 : 0;
-  return up256((size_t)p.total_q * p.hq * 8) + up256(sums);
+  return backward_parts(c, dt).size;
 }
 
 cudaError_t launch_packed_forward(PackedArgs p, void* workspace, na_dtype dt, cudaStream_t st) {
@@ -773,10 +815,22 @@ cudaError_t launch_packed_forward(PackedArgs p, void* workspace, na_dtype dt, cu
 
 cudaError_t launch_packed_backward(PackedArgs p, void* workspace, na_dtype dt, cudaStream_t st) {
   packed_backward_plan(&p, dt);
+  const BackwardParts w = backward_parts(p, dt);
   p.terms = (float2*)workspace;
-  p.part_o = (float*)((char*)workspace + up256((size_t)p.total_q * p.hq * 8));
+  p.part_o = (float*)((char*)workspace + w.sums);
+  const bool lifted = p.path == kPathTc && dt == NA_F16;
+  if (lifted) {
+    p.row_lifts = (float*)((char*)workspace + w.row_lifts);
+    p.lifts = (float*)((char*)workspace + w.lifts);
+  }
   if (p.total_q > 0) {
     cudaError_t e = by_type(dt, [&](auto t) { return terms_t<decltype(t)>(p, st); });
+    if (e != cudaSuccess) return e;
+  }
+  if (lifted) {
+    const long long blocks = (long long)p.nseq * p.hk, most = 148 * 8;
+    packed_lifts_kernel<<<(unsigned)(blocks < most ? blocks : most), 256, 0, st>>>(p);
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   if (p.path == kPathTc) return launch_packed_backward_tc(p, dt, st);

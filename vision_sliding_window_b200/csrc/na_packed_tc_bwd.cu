@@ -26,6 +26,11 @@
 //
 // P and dS are rounded to the input type for their products.  fp16 weights are
 // lifted by 2^15, which leaves them below 2^16 and keeps the bits of small ones.
+// fp16 dS = P (dP - delta) would vanish for gradients of 1e-3 over some thousand
+// keys.  It is lifted by the power of two that brings the norm of dO's row (for
+// dk, whose products sum over rows, of the largest row of the sequence and key
+// head) to 16 to 32, and stays below 2^16 where values' norms are below 2^10,
+// as |dS| <= 2 |dO| |V|; above that the row or key is taken again in float32.
 //
 // delta = dout . out comes from an out that was rounded.  Where all of a row's
 // keys are in one tile (the first rows of a causal sequence, whose out is
@@ -200,7 +205,10 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(raw + C::BAR_OFF + C::TMEM_SLOT);
   const uint32_t s_at = tmem, dp_at = tmem + 128, dv_at = tmem + 256, dk_at = tmem + 256 + D;
+  // log2 of the weights' lift, and what turns dP - delta into the factor that,
+  // times them, is the lifted dS
   constexpr float kLift = BF16 ? 0.f : 15.f, kUnlift = BF16 ? 1.f : 1.f / 32768.f;
+  const float lift = BF16 ? 1.f : p.lifts[(long long)s * p.hk + kh], to_ds = kUnlift * lift;
 
   if (warp < 4) {
     regs_dec<C::REGS_CTRL>();
@@ -227,7 +235,7 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
             if (at < P && pos + at < sp.nq)
               t = p.terms[((long long)sp.q0 + pos + at) * p.hq + kh * p.group + (r - at * p.group)];
             lse[r] = t.x - kLift;
-            lse[kTile + r] = t.y * kUnlift;
+            lse[kTile + r] = t.y * to_ds;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(bar.full_t(i));
@@ -388,8 +396,8 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
           const float4 l = delta[8 * c + e / 4];
           float f[4] = {__uint_as_float(y[c][e]), __uint_as_float(y[c][e + 1]), __uint_as_float(y[c][e + 2]),
                         __uint_as_float(y[c][e + 3])};
-          fma2(f[0], f[1], f[0], f[1], kUnlift, kUnlift, -l.x, -l.y);
-          fma2(f[2], f[3], f[2], f[3], kUnlift, kUnlift, -l.z, -l.w);
+          fma2(f[0], f[1], f[0], f[1], to_ds, to_ds, -l.x, -l.y);
+          fma2(f[2], f[3], f[2], f[3], to_ds, to_ds, -l.z, -l.w);
 #pragma unroll
           for (int u = 0; u < 4; ++u) f[u] *= __uint_as_float(x[c][e + u]);
           w[e / 2] = pack2<T>(f[0], f[1]);
@@ -409,7 +417,7 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     if (ok) {
       tc_fence_after();
       // the first warpgroup writes dv, the second dk
-      const float f0 = half ? p.scale : 1.f, taken = half ? p.scale : kUnlift;
+      const float f0 = half ? p.scale : 1.f, taken = half ? p.scale / lift : kUnlift;
       const uint32_t from = (half ? dk_at : dv_at) + lanes;
       const long long at = ((long long)(sp.k0 + j0 + key) * p.hk + kh) * D;
       T* to = (T*)(half ? p.dk : p.dv) + at;
@@ -640,6 +648,7 @@ packed_dq_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
     visible(p, sp, live ? pos : pos0, &lo, &hi);
     const int all_lo = __reduce_max_sync(0xffffffffu, lo), all_hi = __reduce_min_sync(0xffffffffu, hi);
     float2 term = p.terms[out_row];
+    const float lift = BF16 ? 1.f : p.row_lifts[out_row];
     const float sl2 = p.scale * kLog2e;
     bool ok = true;
     // both warpgroups meet once where n is 1, also when one has given up
@@ -713,7 +722,10 @@ packed_dq_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
           float f0 = __uint_as_float(y[c][e]), f1 = __uint_as_float(y[c][e + 1]);
-          add2(f0, f1, f0, f1, -term.y, -term.y);
+          if constexpr (BF16)
+            add2(f0, f1, f0, f1, -term.y, -term.y);
+          else
+            fma2(f0, f1, f0, f1, lift, lift, -term.y * lift, -term.y * lift);
           f0 *= __uint_as_float(x[c][e]);
           f1 *= __uint_as_float(x[c][e + 1]);
           w[e / 2] = pack2<T>(f0, f1);
@@ -730,6 +742,7 @@ packed_dq_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
       tc_fence_after();
       // each warpgroup writes half of the columns
       constexpr int H = D / 2, W = H < 32 ? H : 32;
+      const float taken = p.scale / lift;
       T* to = (T*)p.dq + out_row * D + half * H;
       bool finite = true;
 #pragma unroll
@@ -739,7 +752,7 @@ packed_dq_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
         float f[W];
 #pragma unroll
         for (int e = 0; e < W; ++e) {
-          f[e] = __uint_as_float(o[e]) * p.scale;
+          f[e] = __uint_as_float(o[e]) * taken;
           finite = finite && fabsf(f[e]) < INFINITY;
         }
         if (live) store_run<T, W>(to + W * c, f);
