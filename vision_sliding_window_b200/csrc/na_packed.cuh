@@ -58,6 +58,16 @@ NA_DEVICE void seen_by(const PackedArgs& p, const Span& s, int j, int* lo, int* 
   }
 }
 
+// Rows of the `per` positions from `pos` on that are a sequence's of nq positions,
+// and where position `at` stands among them.  Positions are cut to the tile
+// before they are multiplied: a sequence's rows may be more than 2^31.
+__host__ __device__ __forceinline__ int rows_of_tile(int nq, int pos, int per, int group) {
+  return (nq - pos < per ? nq - pos : per) * group;
+}
+__host__ __device__ __forceinline__ int row_in_tile(int at, int pos, int per, int group) {
+  return (at < pos ? 0 : at - pos < per ? at - pos : per) * group;
+}
+
 // Keys of a piece of a sequence whose keys are cut: fixed, or its share when
 // every sequence is cut into the same number of pieces.
 NA_DEVICE int piece_length(const PackedArgs& p, const Span& s) {

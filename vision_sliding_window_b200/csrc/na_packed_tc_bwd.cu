@@ -244,7 +244,7 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         const int slots = first_warp ? C::SA : C::SB;
         if (i >= slots && !mbar_wait(empty, ((i / slots) - 1) & 1, ab, p.status)) break;
         if (!load_ring_tile<D>(first_warp ? q_tile(i) : o_tile(i), first_warp ? bar.full_a(i) : bar.full_b(i), bar.tail(),
-                          (sp.nq - pos) * p.group, P * p.group, bytes, ab, p.status, [&](uint32_t dst, uint32_t b) {
+                          rows_of_tile(sp.nq, pos, P, p.group), P * p.group, bytes, ab, p.status, [&](uint32_t dst, uint32_t b) {
                             load_row_tile<D>(dst, first_warp ? &mq : &mo, b, kh, sp.q0 + pos);
                           }))
           break;
@@ -334,7 +334,7 @@ packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
       tc_fence_after();
       const int pos = tile_pos(i);
       const bool masked = pos < all_lo || pos + P > all_hi;
-      const int a = (lo - pos) * p.group - half * 64, b = (min(hi, pos + P) - pos) * p.group - half * 64;
+      const int a = row_in_tile(lo, pos, P, p.group) - half * 64, b = row_in_tile(hi, pos, P, p.group) - half * 64;
       const float4* lse = reinterpret_cast<const float4*>(lse_of(i) + half * 64);
       const float4* delta = lse + kTile / 4;
       uint32_t x[2][32];
