@@ -187,6 +187,26 @@ def check_gradients(q, k, v, dout, cu_q, cu_k, causal=False, window=0, scale=Non
     return got
 
 
+GRADIENTS = [
+    # lq, lk, hq, hk, d, dtype, causal, window
+    ([5, 1, 130, 64], [5, 1, 130, 64], 4, 2, 64, "bf16", True, 0),
+    ([257, 128, 3], [257, 128, 3], 8, 2, 128, "bf16", True, 0),
+    ([300, 17, 511], [300, 17, 511], 6, 2, 64, "f16", False, 0),
+    ([700, 90], [700, 90], 7, 1, 128, "bf16", True, 200),
+    ([100, 33], [612, 333], 4, 4, 128, "f16", True, 0),
+    ([40, 200], [24, 100], 4, 2, 64, "bf16", True, 0),
+    ([129, 255], [129, 255], 3, 3, 16, "f16", True, 0),
+    ([200, 65], [200, 65], 4, 2, 64, "f32", True, 0),
+    ([31, 200], [31, 200], 130, 1, 16, "bf16", True, 0),
+]
+
+
+@pytest.mark.parametrize("lq,lk,hq,hk,d,dtype,causal,window", GRADIENTS)
+def test_gradients_with_the_sum_that_the_kernel_takes(lq, lk, hq, hk, d, dtype, causal, window):
+    q, k, v, cu_q, cu_k, _ = batch(lq, lk, hq, hk, d, dtype, seed=d + hq)
+    check_gradients(q, k, v, batch(lq, lk, hq, hk, d, dtype, seed=99)[0], cu_q, cu_k, causal, window)
+
+
 @pytest.mark.parametrize("size", [1e-3, 1e-4, 2e-6, 3e3])
 @pytest.mark.parametrize("qstd", [0.125, 8.0])
 @pytest.mark.parametrize("causal", [False, True])
@@ -241,3 +261,86 @@ def test_what_a_row_does_not_see_does_not_reach_its_gradients(dtype, bad):
     again = na2d.packed_backward(q, k, v, out, lse, dout, cu_q, cu_k, **kw)
     for a, b, clean in zip(got, again, (rows, keys, keys)):
         assert torch.equal(a[clean], b[clean])
+
+
+def test_many_float16_keys_of_small_weight():
+    """139999 keys of weight e^-17.75 beside one of weight 1: together 0.3%, each
+    below half of float16's smallest step."""
+    n, d = 140000, 64
+    for lq in (1, 40):
+        q = torch.zeros(lq, 1, d, dtype=torch.float16, device="cuda")
+        k, v = (torch.zeros(n, 1, d, dtype=torch.float16, device="cuda") for _ in range(2))
+        q[..., 0] = 1.0
+        k[1:, :, 0] = -17.75
+        v[1:] = 1.0
+        out, lse = na2d.packed_forward(q, k, v, starts([lq]), starts([n]), scale=1.0)
+        synchronized()
+        total = 1.0 + (n - 1) * math.exp(-17.75)
+        want = (total - 1.0) / total
+        # half a step of a weight lifted by 2^7, or of one beside a warp's own largest, is 2^-32; roundings of weights
+        # and of out
+        bound = n * 2.0 ** -32 + 2 * 2.0 ** -11 * want
+        assert (out.double() - want).abs().max().item() <= bound
+        assert (lse.double() - math.log(total)).abs().max().item() <= 1e-5
+
+
+# ------------------------------------- long sequences in the kernel for few rows
+LONG_AMONG_FEW = [
+    # lq, lk, hq, hk, d, dtype, causal, window: 16 rows (of a group) a sequence on average
+    ([17, 90, 400] + [1] * 60, [17, 1200, 400] + [33 * i + 1 for i in range(60)], 2, 2, 64, "bf16", True, 0),
+    ([17, 90, 400] + [1] * 60, [300, 90, 700] + [33 * i + 1 for i in range(60)], 4, 4, 128, "f16", True, 100),
+    ([1] * 40 + [37, 150], [65] * 40 + [2000, 150], 6, 3, 32, "bf16", False, 0),
+    ([130, 0, 5] + [1] * 30, [64, 9, 0] + [700] * 30, 4, 2, 16, "f16", True, 0),       # rows without keys, no rows
+    ([40, 1, 1, 1, 20], [9000, 5000, 6000, 12, 4097], 1, 1, 128, "bf16", True, 0),     # keys cut into pieces
+    ([33, 1, 1], [9000, 5001, 40], 2, 2, 64, "f16", False, 0),
+    ([40, 1, 1, 1, 20], [9000, 5000, 6000, 12, 4097], 1, 1, 128, "bf16", True, 4500),
+    ([60] + [1] * 9, [2000] + [1500] * 9, 2, 1, 64, "f32", True, 0),                   # float32, in pieces
+    ([50] + [1] * 9, [900] + [2500] * 9, 4, 2, 16, "f32", False, 0),
+]
+
+
+@pytest.mark.parametrize("lq,lk,hq,hk,d,dtype,causal,window", LONG_AMONG_FEW)
+@pytest.mark.parametrize("extra", [0, 3])
+def test_long_sequences_among_single_tokens(lq, lk, hq, hk, d, dtype, causal, window, extra):
+    assert (sum(lq) + extra) * (hq // hk) <= 16 * len(lq)
+    q, k, v, cu_q, cu_k, _ = batch(lq, lk, hq, hk, d, dtype, seed=len(lq), extra=extra)
+    out, lse = torch.full_like(q, 7.0), torch.full((hq, len(q)), 7.0, device="cuda")
+    na2d.packed_forward(q, k, v, cu_q, cu_k, causal=causal, window=window, out=out, lse=lse)
+    synchronized()
+    want, wlse, tol, ltol = plain64.forward(q, k, v, cu_q, cu_k, causal=causal, window=window)
+    plain64.check("out", out, want, tol)
+    plain64.check("lse", lse, wlse, ltol)
+    n = sum(lq)
+    assert (out[n:] == 7).all() and (lse[:, n:] == 7).all()
+
+
+# --------------------------------------------------------------- lying lengths
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("lq,lk", [([64, 100], [64, 100]), ([1, 1], [1, 1]), ([3, 1], [9000, 40]), ([70, 9], [2600, 30])])
+def test_lengths_that_lie_write_nothing_outside(dtype, lq, lk):
+    """Everything that a call writes lies between rows of a pattern that must stay."""
+    q, k, v, cu_q, cu_k, _ = batch(lq, lk, 4, 2, 64, dtype, seed=13)
+    inside = []
+
+    def guarded(shape, t):
+        n = math.prod(shape)
+        whole = torch.full((n + 2 * 4096,), 7.0, dtype=t, device="cuda")
+        inside.append((whole, n))
+        return whole[4096:4096 + n].view(shape)
+
+    out, lse = guarded(q.shape, q.dtype), guarded((4, len(q)), torch.float32)
+    grads = [guarded(t.shape, t.dtype) for t in (q, k, v)]
+    sizes = (len(lq), len(q), len(k), 4, 2, 64, {"f32": 0, "f16": 1, "bf16": 2}[dtype])
+    lib = na2d.load_library()
+    ws = guarded((max(lib.na_packed_workspace_bytes(*sizes), 256) // 4,), torch.float32)
+    back = guarded((max(lib.na_packed_backward_workspace_bytes(*sizes), 256) // 4,), torch.float32)
+    far = torch.tensor([2 ** 31 - 1, -5], dtype=torch.int32, device="cuda")
+    for a, b in ((cu_q + 1000000, cu_k), (cu_q, cu_k + 1000000), (cu_q - 5000, cu_k - 5000), (cu_q, cu_k * 5),
+                 (cu_q.flip(0).contiguous(), cu_k.flip(0).contiguous()), (cu_q * 7, cu_k * 5), (cu_q * 0, cu_k)):
+        for causal in (False, True):
+            na2d.packed_forward(q, k, v, a, b, far, causal=causal, out=out, lse=lse, workspace=ws)
+            na2d.packed_backward(q, k, v, torch.zeros_like(q), torch.zeros_like(lse), q, a, b, causal=causal, grads=grads,
+                                 workspace=back)
+            synchronized()
+            for whole, n in inside:
+                assert (whole[:4096] == 7).all() and (whole[4096 + n:] == 7).all()
