@@ -286,7 +286,7 @@ na_status na_packed_backward(const void *q, const void *k, const void *v, const 
  * x and h may be o (a call reads a row before it writes it); no other
  * overlaps.  Statistics are float32, and h comes from y before its rounding to
  * dt.  rows * C < 2^40, C <= 8192 (more: NA_ERR_UNSUPPORTED).  rows = 0 is a
- * no-op.
+ * no-op, whatever the pointers.
  */
 na_status na_norm_forward(const void *x, const void *o, const void *post_w, const void *post_b, const void *gate,
                           const void *w, const void *b, void *y, void *h, long long rows, int C, long long gates,

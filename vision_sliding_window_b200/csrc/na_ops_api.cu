@@ -153,10 +153,9 @@ NA_EXPORT na_status na_norm_forward(const void* x, const void* o, const void* po
   NormArgs p;
   const na_status st = check_norm(rows, C, gates, rms, post, eps, scale, dt, &p);
   if (st != NA_OK) return st;
-  if (gates > 0 && !gate && rows > 0) return NA_ERR_INVALID_ARG;
-  if (gate && gates == 0) return NA_ERR_INVALID_ARG;
+  if (rows == 0) return NA_OK;  // whatever the pointers: those of empty buffers may be NULL
+  if ((gate != nullptr) != (gates > 0)) return NA_ERR_INVALID_ARG;
   if ((!o && (post || gate)) || (!post && (post_w || post_b)) || (!h && (w || b))) return NA_ERR_INVALID_ARG;
-  if (rows == 0) return NA_OK;
   if ((o != nullptr) != (y != nullptr) || (!y && !h)) return NA_ERR_INVALID_ARG;  // without o, y is x
   if (bad(x, true)) return NA_ERR_INVALID_ARG;
   for (const void* ptr : {o, post_w, post_b, gate, w, b, (const void*)y, (const void*)h})
