@@ -503,7 +503,7 @@ def norm_backward(y, dh, dy=None, w=None, b=None, o=None, post: bool = False, po
                   scale: float = 1.0, eps: float = 1e-5, rms: bool = False, workspace=None) -> NormGrads:
     """Gradients through norm_forward (na_norm_backward), y its first result and
     dh, dy the gradients of both (None: zero).  dx and do have x's type, the
-    others are float32 (dgate of gate's shape)."""
+    others are float32 (dgate of gate's shape), zeros where there are no rows."""
     rows, C, gates = _norm_dims(y, o, post, post_w, post_b, gate, w, b)
     if dh is None and (dy is None or w is not None or b is not None):
         raise ValueError("dh is missing: give dy instead, without w and b")
@@ -521,6 +521,11 @@ def norm_backward(y, dh, dy=None, w=None, b=None, o=None, post: bool = False, po
     g = NormGrads(torch.empty_like(y), None if o is None else torch.empty_like(y),
                   *(next(rest) if there else None for there in given),
                   None if gate is None else torch.empty(gate.shape, device=y.device, dtype=torch.float32))
+    if rows == 0:  # which the library refuses: its kernels would leave the sums unwritten
+        for t in g:
+            if t is not None:
+                t.zero_()
+        return g
     dt = _DT[y.dtype]
     workspace, size = _workspace(workspace, _bytes_for("na_norm_backward_workspace_bytes", rows, C, gates, dt), y)
     _enqueue(y, "na_norm_backward", (y, o, post_w, post_b, gate, w, dy, dh, *g, workspace), size, rows, C, gates,
