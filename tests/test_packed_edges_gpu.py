@@ -344,3 +344,44 @@ def test_lengths_that_lie_write_nothing_outside(dtype, lq, lk):
             synchronized()
             for whole, n in inside:
                 assert (whole[:4096] == 7).all() and (whole[4096 + n:] == 7).all()
+
+
+# ------------------------------------------------- numbers longer than 32 bits
+def test_windows_of_more_than_32_bits():
+    for dtype in ("bf16", "f32"):
+        q, k, v, cu_q, cu_k, _ = batch([200, 9], [200, 9], 2, 2, 64, dtype, seed=41)
+        want, lse = na2d.packed_forward(q, k, v, cu_q, cu_k, causal=True)
+        grads = na2d.packed_backward(q, k, v, want, lse, q, cu_q, cu_k, causal=True)
+        for window in (2 ** 31 - 1, 2 ** 31, 2 ** 32 + 5, 10 ** 30):
+            assert torch.equal(na2d.packed_forward(q, k, v, cu_q, cu_k, causal=True, window=window)[0], want)
+            got = na2d.packed_backward(q, k, v, want, lse, q, cu_q, cu_k, causal=True, window=window)
+            assert all(torch.equal(a, b) for a, b in zip(got, grads))
+        for window in (-1, -2 ** 31 - 1, -2 ** 32):
+            with pytest.raises(na2d.NA2DError):
+                na2d.packed_forward(q, k, v, cu_q, cu_k, causal=True, window=window)
+    synchronized()
+
+
+def test_sizes_of_more_than_32_bits_are_refused():
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("needs 12 GB of free device memory")
+    q = torch.empty(1, 1, 2 ** 32 + 16, dtype=torch.bfloat16, device="cuda")
+    cu = starts([1])
+    for call in (lambda: na2d.packed_forward(q, q, q, cu, cu),
+                 lambda: na2d.packed_backward(q, q, q, q, torch.zeros(1, 1, device="cuda"), q, cu, cu, grads=(q, q, q)),
+                 lambda: na2d.norm_forward(q, h=q), lambda: na2d.norm_backward(q, q)):
+        with pytest.raises(na2d.NA2DError) as e:
+            call()
+        assert e.value.status == na2d.NA_ERR_UNSUPPORTED
+    synchronized()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_calls_without_rows_keys_or_sequences(dtype):
+    for lq, lk, hq, hk in (([], [], 2, 1), ([0, 0], [5, 300], 4, 2), ([3, 70], [0, 0], 2, 2), ([0], [0], 1, 1)):
+        q, k, v, cu_q, cu_k, _ = batch(lq, lk, hq, hk, 64, dtype)
+        out, lse = check_forward(q, k, v, cu_q, cu_k, causal=True)
+        assert (out == 0).all() and (lse == -math.inf).all()
+        grads = na2d.packed_backward(q, k, v, out, lse, q, cu_q, cu_k, causal=True)
+        synchronized()
+        assert all((g == 0).all() for g in grads)

@@ -325,6 +325,19 @@ def _enqueue(like, name, tensors, *numbers):
         raise NA2DError(status, name)
 
 
+_INT_MAX = 2 ** 31 - 1  # ctypes cuts longer numbers without a word
+
+
+def _sizes_fit(name, sizes):
+    if max(sizes) > _INT_MAX:
+        raise NA2DError(NA_ERR_UNSUPPORTED, name)
+
+
+def _window(n) -> int:
+    """A window of more keys than there can be sees as many; a negative one stays so."""
+    return max(min(int(n), _INT_MAX), -1)
+
+
 def _raw_stream(device: int) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
@@ -382,6 +395,7 @@ def packed_forward(q, k, v, cu_q, cu_k, len_k=None, causal: bool = False, window
     defaults to d ** -0.5.  Rows of no sequence are not written: what a tensor
     that this call allocates holds there is not defined."""
     dims = _packed_dims(q, k, v, cu_q, cu_k, len_k)
+    _sizes_fit("na_packed_forward", dims)
     nseq, tq, _, hq, _, d = dims
     if out is None:
         out = torch.empty_like(q)
@@ -399,7 +413,7 @@ def packed_forward(q, k, v, cu_q, cu_k, len_k=None, causal: bool = False, window
     if need or workspace is not None:
         workspace, size = _workspace(workspace, need, q)
     _enqueue(q, "na_packed_forward", (q, k, v, cu_q, cu_k, len_k, out, lse, workspace), size, *dims, int(causal),
-             int(window), d ** -0.5 if scale is None else float(scale), dt)
+             _window(window), d ** -0.5 if scale is None else float(scale), dt)
     return out, lse
 
 
@@ -409,6 +423,7 @@ def packed_backward(q, k, v, out, lse, dout, cu_q, cu_k, causal: bool = False, w
     dv), written into `grads` where given.  out and lse are the forward's;
     rows of no sequence are not written."""
     dims = _packed_dims(q, k, v, cu_q, cu_k, None)
+    _sizes_fit("na_packed_backward", dims)
     nseq, tq, _, hq, _, d = dims
     _need_all(q, q.dtype, out=out, dout=dout)
     _need_all(q, torch.float32, lse=lse)
@@ -423,7 +438,7 @@ def packed_backward(q, k, v, out, lse, dout, cu_q, cu_k, causal: bool = False, w
     dt = _DT[q.dtype]
     workspace, size = _workspace(workspace, _bytes_for("na_packed_backward_workspace_bytes", *dims, dt), q)
     _enqueue(q, "na_packed_backward", (q, k, v, out, lse, dout, cu_q, cu_k, dq, dk, dv, workspace), size, *dims,
-             int(causal), int(window), d ** -0.5 if scale is None else float(scale), dt)
+             int(causal), _window(window), d ** -0.5 if scale is None else float(scale), dt)
     return dq, dk, dv
 
 
@@ -471,6 +486,7 @@ def norm_forward(x, w=None, b=None, o=None, post: bool = False, post_w=None, pos
     [gates, C] (each row for an equal share of consecutive rows) or None.
     o=None: y is x itself.  norm=False: only y, and h is None."""
     rows, C, gates = _norm_dims(x, o, post, post_w, post_b, gate, w, b)
+    _sizes_fit("na_norm_forward", (C,))
     if not norm and (w is not None or b is not None or h is not None or o is None):
         raise ValueError("norm=False takes o, and neither w, b nor h")
     if o is None and y is not None:
@@ -505,6 +521,7 @@ def norm_backward(y, dh, dy=None, w=None, b=None, o=None, post: bool = False, po
     dh, dy the gradients of both (None: zero).  dx and do have x's type, the
     others are float32 (dgate of gate's shape), zeros where there are no rows."""
     rows, C, gates = _norm_dims(y, o, post, post_w, post_b, gate, w, b)
+    _sizes_fit("na_norm_backward", (C,))
     if dh is None and (dy is None or w is not None or b is not None):
         raise ValueError("dh is missing: give dy instead, without w and b")
     _need_all(y, y.dtype, dh=dh, dy=dy)
@@ -553,6 +570,7 @@ def layer_forward(x, w, b, wqkv, bqkv, wo, bo, rpb, heads: int, ksize: int, gate
     _need_all(x, x.dtype, y=y)
     _need_shape(y, "y", x.shape)
     dt, dims = _DT[x.dtype], (B, H, W, heads, C // heads, ksize)
+    _sizes_fit("na2d_layer_forward", (*dims, gates))
     workspace, size = _workspace(workspace, _bytes_for("na2d_layer_workspace_bytes", *dims, dt), x)
     _enqueue(x, "na2d_layer_forward", (x, w, b, wqkv, bqkv, wo, bo, rpb, post_w, post_b, gate, y, workspace), size,
              *dims, gates, int(rms), int(post), float(eps), float(scale), dt)
