@@ -222,17 +222,25 @@ na_status na_forward_nd(const void *q, const void *k, const void *v, const void 
  *   lse[h][i] = ln sum_j e^(s_ij), float32 [heads_q][total_q] (NULL: not written).
  *
  * A row that sees no key gets zeros and an lse of -inf, and so does one whose
- * logits are all -inf.  Keys that a row does
- * not see, slots past len_k and other sequences never reach its result,
- * whatever they hold (NaN and infinities too).  Rows of q that belong to no
- * sequence are left as they were in out and lse.  The lengths are read on the
- * device and clamped to the tensors, so a captured call can be replayed with
- * other lengths in the same buffers.
+ * logits are all -inf.  Keys that a row does not see, slots past len_k and other
+ * sequences never reach its result, whatever they hold (NaN and infinities too).
+ * Rows of q that belong to no sequence are left as they were in out and lse.
+ *
+ * The lengths are read on the device and clamped to the tensors, so a captured
+ * call can be replayed with other lengths in the same buffers.  Which kernel
+ * runs, and how work is split, follows from the sizes given: at most 16 rows (of
+ * a group) a sequence on average make a call of few rows, whose kernel walks a
+ * longer sequence 16 rows at a time - right, but a long prompt among single
+ * tokens is faster in a call of its own.
  *
  * Softmax statistics and sums are float32; 16-bit types round the weights to
- * dt for the weighted sum.  d in {16, 32, 64, 128}; scale > 0; window >= 0,
- * and 0 unless causal; total_q, total_k <= 2^30, heads_k <= 65535 and
- * (total_q + total_k) * heads_q * d < 2^40 (more: NA_ERR_UNSUPPORTED).
+ * dt for the weighted sum.  In the 16-bit types rows (and, in the backward pass,
+ * keys) whose result is not finite are computed a second time, entry by entry,
+ * which is slow: a NaN that a whole sequence sees costs many times a call.
+ *
+ * d in {16, 32, 64, 128}; scale > 0; window >= 0, and 0 unless causal; total_q,
+ * total_k <= 2^30, heads_k <= 65535 and (total_q + total_k) * heads_q * d < 2^40
+ * (more: NA_ERR_UNSUPPORTED).
  * workspace: a 256-byte aligned device buffer of at least na_packed_workspace_bytes() bytes (may be
  * 0); calls that may run at the same time need one each.
  * NULL is allowed for k and v when total_k is 0.
@@ -252,8 +260,7 @@ na_status na_packed_forward(const void *q, const void *k, const void *v, const i
  *
  * dk and dv summed over the heads of the group too (where a row's keys are few,
  * sum_j P_ij dout_i . v_j stands for dout_i . out_i, which it equals but for
- * out's rounding).  Arguments as the
- * forward's; every key slot belongs to the sequence (there is no len_k).
+ * out's rounding).  Arguments as the forward's; every key slot belongs to the sequence (there is no len_k).
  * dq, dk and dv are written, not added to; rows of no sequence are left as
  * they were.  16-bit types round P and dS to dt for their products; fp16 ones
  * are lifted by powers of two first (dS by dout's norm), so that small ones keep

@@ -20,6 +20,7 @@
 // deviations from it, which is exact to rounding whatever the mean is, as "sum
 // of squares minus squared sum" is not.  Backward: sums over differences from a
 // few of the row's own values, see backward_row.
+#include <atomic>
 #include <type_traits>
 
 #include "na2d_common.cuh"
@@ -81,6 +82,10 @@ template <typename T, int VEC> NA_DEVICE Pack<T, VEC> load_row(const T* p) {
 // takes 40; then one 16-byte load a lane reads all warps' sums.  `slot`
 // alternates between two areas of shared memory, so that one barrier a
 // reduction is enough.
+//
+// All lanes of a warp, or all threads of a block, call sum() together, also for
+// rows that are not theirs to write: several rows share a warp, and a sum that
+// only some rows take would shuffle with lanes that are not there.
 constexpr int kMaxWarps = 16, kMaxSums = 8;
 
 struct Reducer {
@@ -995,11 +1000,12 @@ int ring_stages(size_t stage_bytes, int blocks_per_sm) {
 
 // ---------------------------------------------------------------- launches
 int sms() {
-  static int counts[64] = {};
+  static std::atomic<int> counts[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-  if (!counts[dev]) cudaDeviceGetAttribute(&counts[dev], cudaDevAttrMultiProcessorCount, dev);
-  return counts[dev] > 0 ? counts[dev] : 148;
+  int n = counts[dev];
+  if (n == 0 && cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess) counts[dev] = n;
+  return n > 0 ? n : 148;
 }
 
 int pow2_at_least(int n) {

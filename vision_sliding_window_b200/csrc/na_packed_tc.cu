@@ -350,8 +350,8 @@ packed_forward_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_co
           }
         }
       };
-      // Three eighths of the exponentials by polynomial, but not where masked
-      // places must give exactly 0.
+      // A quarter of the exponentials by polynomial, but not where masked places
+      // must give exactly 0.
       if (masked)
         weights(std::false_type{});
       else
