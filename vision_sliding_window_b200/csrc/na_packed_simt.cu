@@ -409,22 +409,28 @@ template <typename T, int D> __global__ void __launch_bounds__(256) packed_terms
   }
 }
 
-// The lift of a sequence's rows of one key head: that of its largest row.
-__global__ void __launch_bounds__(256) packed_lifts_kernel(PackedArgs p) {
-  __shared__ float least[8];
+// The lift of a sequence's rows of one key head: that of its largest row.  A
+// thread keeps to one head of the group (there are 128 at most here), so that
+// nothing is divided between the loads, which are what this waits for.
+constexpr int kLiftThreads = 512;
+__global__ void __launch_bounds__(kLiftThreads) packed_lifts_kernel(PackedArgs p) {
+  __shared__ float least[kLiftThreads / 32];
+  const int per = kLiftThreads / p.group, at = threadIdx.x / p.group, g = threadIdx.x % p.group;
   for (long long u = blockIdx.x; u < (long long)p.nseq * p.hk; u += gridDim.x) {
     const Span sp = span_of(p, (int)(u / p.hk));
     const int kh = (int)(u % p.hk);
     float f = kMostLift;
-    for (long long r = threadIdx.x; r < (long long)sp.nq * p.group; r += 256)
-      f = fminf(f, p.row_lifts[(sp.q0 + r / p.group) * p.hq + kh * p.group + r % p.group]);
+    const float* from = p.row_lifts + (long long)sp.q0 * p.hq + kh * p.group + g;
+    if (at < per)
+#pragma unroll 8
+      for (int i = at; i < sp.nq; i += per) f = fminf(f, from[(long long)i * p.hq]);
     f = -warp_max(-f);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) least[threadIdx.x >> 5] = f;
     __syncthreads();
     if (threadIdx.x == 0) {
 #pragma unroll
-      for (int w = 1; w < 8; ++w) f = fminf(f, least[w]);
+      for (int w = 1; w < kLiftThreads / 32; ++w) f = fminf(f, least[w]);
       p.lifts[u] = f;
     }
   }
@@ -829,7 +835,7 @@ cudaError_t launch_packed_backward(PackedArgs p, void* workspace, na_dtype dt, c
   }
   if (lifted) {
     const long long blocks = (long long)p.nseq * p.hk, most = 148 * 8;
-    packed_lifts_kernel<<<(unsigned)(blocks < most ? blocks : most), 256, 0, st>>>(p);
+    packed_lifts_kernel<<<(unsigned)(blocks < most ? blocks : most), kLiftThreads, 0, st>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
