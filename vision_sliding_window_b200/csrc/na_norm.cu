@@ -9,7 +9,7 @@
 // A row lives in registers between its one read and its one write, so the
 // forward pass moves x, o, y and h once each and the backward pass y, o, dy,
 // dh, dx and do once each.  HBM would bound both (82 us and 61 us at 16387 and
-// 8168 rows of 4096, bf16, both norms and a gate); what they take, 105 and 156
+// 8168 rows of 4096, bf16, both norms and a gate); what they take, 104 and 151
 // us, goes to instruction issue and to the waits of the reductions between a
 // row's steps.  So arithmetic is in pairs (two float32 an instruction), weights
 // stay in registers, rows that fill their threads have kernels without a
@@ -853,9 +853,9 @@ __device__ __noinline__ void ring_settle(uint32_t bars, int it, int stages) {
 }
 
 // Blocks of 256 threads an SM: with weights held (16 bits) registers leave room
-// for two; a third spills, and costs 112 us where two take 106 (16387 rows of
-// 4096).  float32 reads its weights again and has three, 108 us for 143 (8000
-// rows of 2500).
+// for two; a third spills, and costs 112 us where two take 104 (16387 rows of
+// 4096).  float32 reads its weights again and has three, 80 us where two take 98
+// (8000 rows of 2500).
 template <typename T> constexpr int kWideBlocks = sizeof(T) == 2 ? 2 : 3;
 
 template <typename T, int VEC, int NV, int THREADS, bool FULL>
