@@ -238,12 +238,12 @@ na_status na_forward_nd(const void *q, const void *k, const void *v, const void 
  * keys) whose result is not finite are computed a second time, entry by entry,
  * which is slow: a NaN that a whole sequence sees costs many times a call.
  *
- * d in {16, 32, 64, 128}; scale > 0; window >= 0, and 0 unless causal; total_q,
- * total_k <= 2^30, heads_k <= 65535 and (total_q + total_k) * heads_q * d < 2^40
- * (more: NA_ERR_UNSUPPORTED).
- * workspace: a 256-byte aligned device buffer of at least na_packed_workspace_bytes() bytes (may be
- * 0); calls that may run at the same time need one each.
- * NULL is allowed for k and v when total_k is 0.
+ * What is written overlaps nothing that is read.  d in {16, 32, 64, 128};
+ * scale > 0; window >= 0, and 0 unless causal; total_q, total_k <= 2^30,
+ * heads_k <= 65535 and (total_q + total_k) * heads_q * d < 2^40 (more:
+ * NA_ERR_UNSUPPORTED).  workspace: a 256-byte aligned device buffer of at least
+ * na_packed_workspace_bytes() bytes (may be 0); calls that may run at the same
+ * time need one each.  NULL is allowed for k and v when total_k is 0.
  */
 size_t na_packed_workspace_bytes(int nseq, int total_q, int total_k, int heads_q, int heads_k, int d, na_dtype dt);
 na_status na_packed_forward(const void *q, const void *k, const void *v, const int *cu_q, const int *cu_k,

@@ -233,6 +233,14 @@ def test_float16_gradients_of_rows_of_zeros_and_of_all_sizes():
     assert all((g == 0).all() for g in grads)
 
 
+def test_float16_values_so_large_that_a_lifted_gradient_overflows():
+    """Norms of 8000 along dout: |dS| reaches 2^17 before it is taken again in float32."""
+    lens = [2, 3, 200]
+    q, k, v, cu_q, cu_k, _ = batch(lens, lens, 2, 2, 64, "f16", seed=25)
+    v = (v.float() * 1000).half()
+    check_gradients(q, k, v, (v.float() * 1e-5).half(), cu_q, cu_k)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("bad", [40, 200])
 def test_what_a_row_does_not_see_does_not_reach_its_gradients(dtype, bad):

@@ -96,7 +96,7 @@ class Block:
         return True
 
     def run(self):
-        hardware = self.rnd.random()
+        hardware, idle = self.rnd.random(), 0
         while self.roles:
             if self.rnd.random() < 0.05:  # someone falls asleep or wakes
                 self.rnd.choice(self.roles)[0] = self.rnd.random()
@@ -116,8 +116,12 @@ class Block:
                     self.roles.remove(r)
                     break
             else:
-                if not self.fire():
+                # a role that came to its next wait has perhaps let an earlier one go on
+                idle = 0 if self.fire() else idle + 1
+                if idle > len(self.roles) + 1:
                     raise Stuck("deadlock: " + ", ".join(r[1] for r in self.roles))
+                continue
+            idle = 0
         while self.fire():
             pass
 
@@ -363,6 +367,168 @@ def dkdv(n, seed, sa, sb, tail, s_slots, dp_slots, half_slots, p_slots, ds_slots
         block.role(f"softmax {w}", softmax(w))
     block.run()
     expect(sums, [n, n], "steps summed")
+
+
+def forward(steps, seed, slots=4):
+    """The forward: a row tile for each of `steps`, which counts its key tiles; one
+    S that the tiles use in turn, a ring of K_0, V_0, K_1, V_1, ..."""
+    block, n = Block(seed), max(steps)
+    full, empty = InTurn("full", slots), InTurn("empty", slots)
+    s, pv = [InTurn("s", 1) for _ in steps], [InTurn("pv", 1) for _ in steps]
+    p = [[InTurn("p", 1, WARPS) for _ in range(2)] for _ in steps]
+    free, kept = InTurn("free", 1, WARPS), Barrier("q")
+    ring, S, readers = [None] * slots, [None], [0]
+    P, O, written = [[None, None] for _ in steps], [0 for _ in steps], {}
+
+    def loader():
+        block.load(kept.arrive)
+        for i in range(2 * n):
+            if i >= slots:
+                yield from empty.wait(i - slots)
+
+            def land(i=i):
+                ring[i % slots] = i
+                full.arrive(i)
+            block.load(land)
+            yield True
+
+    def products_s():
+        while not kept.passed(0):
+            yield False
+        made = 0
+        for j in range(n):
+            yield from full.wait(2 * j)
+            for t, k in enumerate(steps):
+                if j >= k:
+                    continue
+                if made:
+                    yield from free.wait(made - 1)
+                made += 1
+
+                def product(t=t, j=j):
+                    expect(ring[2 * j % slots], 2 * j, "S's keys")
+                    expect(readers[0], 0, "warps that still read S")
+                    S[0], readers[0] = (t, j), WARPS
+                block.issue("S", product)
+                block.issue("S", lambda t=t, j=j: s[t].arrive(j))
+                yield True
+            block.issue("S", lambda j=j: empty.arrive(2 * j))
+
+    def products_pv():
+        for j in range(n):
+            yield from full.wait(2 * j + 1)
+            for t, k in enumerate(steps):
+                if j >= k:
+                    continue
+                for half in range(2):
+                    yield from p[t][half].wait(j)
+
+                    def product(t=t, j=j, half=half):
+                        expect(ring[(2 * j + 1) % slots], 2 * j + 1, "the values")
+                        expect(P[t][half], j, "the weights")
+                        O[t] += half
+                    block.issue("PV", product)
+                    yield True
+                block.issue("PV", lambda t=t, j=j: pv[t].arrive(j))
+            block.issue("PV", lambda j=j: empty.arrive(2 * j + 1))
+
+    def softmax(t, w):
+        for j in range(steps[t]):
+            yield from s[t].wait(j)
+            expect(S[0], (t, j), "softmax's S")
+            yield True
+            readers[0] -= 1
+            free.arrive(0)
+            if j:
+                yield from pv[t].wait(j - 1)
+                expect(O[t], j, "products before O is rescaled")
+            for half in range(2):
+                yield True
+                written[t, j, half] = written.get((t, j, half), 0) + 1
+                if written[t, j, half] == WARPS:
+                    P[t][half] = j
+                p[t][half].arrive(j)
+        if steps[t]:
+            yield from pv[t].wait(steps[t] - 1)
+            expect(O[t], steps[t], "products at the end")
+
+    block.role("loader", loader())
+    block.role("S", products_s())
+    block.role("PV", products_pv())
+    for t in range(len(steps)):
+        for w in range(WARPS):
+            block.role(f"softmax {t} {w}", softmax(t, w))
+    block.run()
+
+
+def few_rows(tiles, seed, slots):
+    """The kernel for few rows: row tiles of `tiles` key tiles each go through one
+    ring; all warps meet between them, as the join's sums take the ring's place."""
+    block = Block(seed)
+    full, empty = InTurn("full", slots), InTurn("empty", slots, WARPS)
+    ring, met, reading = [None] * slots, [0], [0]
+
+    def meet(k):
+        met[0] += 1
+        while met[0] < k * (WARPS + 1):
+            yield False
+
+    def loader():
+        done = 0
+        for k, n in enumerate(tiles):
+            for u in range(done, done + n):
+                if u >= slots:
+                    yield from empty.wait(u - slots)
+
+                def land(u=u):
+                    expect(ring[u % slots] in ("sums", None, u - slots), True, "a slot that is loaded over")
+                    ring[u % slots] = u
+                    full.arrive(u)
+                block.load(land)
+                yield True
+            for u in range(max(done, done + n - slots), done + n):  # settles
+                yield from full.wait(u)
+            done += n
+            yield from meet(2 * k + 1)
+            yield from meet(2 * k + 2)
+
+    def warp(w):
+        done = 0
+        for k, n in enumerate(tiles):
+            for u in range(done, done + n):
+                yield from full.wait(u)
+                expect(ring[u % slots], u, "a warp's tile")
+                yield True
+                empty.arrive(u)
+            done += n
+            reading[0] += 1
+            while reading[0] < (k + 1) * WARPS:  # all warps have read the ring
+                yield False
+            expect(block.loads, [], "copies in flight over the sums")
+            for i in range(slots):
+                ring[i] = "sums"
+            yield from meet(2 * k + 1)
+            expect(set(ring), {"sums"}, "the sums when they are read")
+            yield True
+            yield from meet(2 * k + 2)
+
+    block.role("loader", loader())
+    for w in range(WARPS):
+        block.role(f"warp {w}", warp(w))
+    block.run()
+
+
+@pytest.mark.parametrize("steps", [(1,), (2,), (7,), (1, 1), (1, 2), (5, 5), (5, 6), (0, 3), (4, 0)])
+def test_forward(steps):
+    for seed in range(150):
+        forward(steps, seed)
+
+
+@pytest.mark.parametrize("slots", [1, 3, 8])
+@pytest.mark.parametrize("tiles", [(1,), (9,), (3, 0, 5), (1, 2, 3, 4), (0, 0, 2), (20, 20)])
+def test_few_rows(tiles, slots):
+    for seed in range(100):
+        few_rows(tiles, seed, slots)
 
 
 RINGS = [(3, 2), (4, 4)]  # slots of the two rings at d = 128 and below
