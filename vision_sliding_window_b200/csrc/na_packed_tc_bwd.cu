@@ -16,7 +16,9 @@
 // needs no further sum.
 //
 // P^T and dS^T are written over S^T and dP^T (16 bits) and read as operands
-// from tensor memory.  The products are issued so that the tensor pipe always
+// from tensor memory; the next S^T and dP^T are written over those by the thread
+// that issued their products before, as one thread's products run in order.  The
+// products are issued so that the tensor pipe always
 // has one while a half of the element-wise work runs: dV and the next S^T
 // beside dS^T, dK and the next dP^T beside P^T.  Two warpgroups share a tile,
 // each 64 of its columns, a thread a lane.  The tiles that are walked come
